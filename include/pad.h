@@ -303,6 +303,142 @@ pad_status pad_decode_tcgen05(const pad_tensor *q, const pad_tensor *k_cache, co
                               int32_t num_splits, pad_tensor *out, pad_tensor *lse, void *stream);
 
 /*
+ * pad_qk_norm_rope -- RMS norm of every head of q and k and the position
+ * rotation, in one pass: what a model does to the projections' rows before
+ * pad_decode reads them.  The source pages have no counterpart.
+ *   n = x * rsqrt(mean(x^2) + eps) * weight        (per head; without a weight n = x)
+ *   (y1, y2) = (n1 cos a - n2 sin a, n2 cos a + n1 sin a),  a = positions[t] * inv_freq[i]
+ * over the first R = 2 * len(inv_freq) elements of a row, the rest passing
+ * through; pair i is elements (i, i + R/2), or (2i, 2i + 1) when `interleaved`.
+ * fp32 arithmetic (the angle's product and reduction in fp64), one rounding.
+ *
+ *  q, k          bf16 [T, Hq, D] and [T, Hkv, D], last dim contiguous, rows 16-byte
+ *                aligned, any other strides (slices of a fused projection); k may
+ *                be NULL (then k_out and k_weight are too).
+ *  q_weight,     bf16 or fp32 [D], NULL = that tensor is not normed.
+ *  k_weight
+ *  eps           finite, >= 0.
+ *  positions     int32 [T], any values; inv_freq fp32 [R/2].  Both NULL = no rotation.
+ *  q_out, k_out  bf16, the shapes of q and k, own strides; each may be its input
+ *                itself (same data and strides), and otherwise overlaps nothing.
+ *
+ * D in {64, 128, 256}; R/2 a multiple of 8, at most D/2; up to 65536 heads.
+ * Asynchronous on `stream`, no scratch, capturable from the first call.
+ */
+pad_status pad_qk_norm_rope(const pad_tensor *q, const pad_tensor *k, const pad_tensor *q_weight,
+                            const pad_tensor *k_weight, float eps, const pad_tensor *positions,
+                            const pad_tensor *inv_freq, int32_t interleaved, pad_tensor *q_out,
+                            pad_tensor *k_out, void *stream);
+
+/*
+ * Options of pad_append_kv.  Zero-initialised: rows are stored as they are.
+ *   inv_freq,     the rotation of pad_qk_norm_rope, applied to K (and q) at
+ *   interleaved   `positions`.
+ *   k_weight, eps the norm of pad_qk_norm_rope, applied to K before its rotation.
+ *   q, q_weight,  query rows of the same tokens, bf16 [T, Hq, D]: normed (with
+ *   q_out         q_weight and eps) and rotated into q_out by the same launch.
+ *   k_scale,      an E4M3 cache holds x / scale, rounded to nearest even, beyond
+ *   v_scale       +-448 as +-448, NaN as NaN.  0 reads as 1; a bf16 cache takes
+ *                 0 or 1 only.  Pass the same scales to pad_decode_ex.
+ */
+typedef struct pad_append_options {
+  const pad_tensor *inv_freq;
+  int32_t interleaved;
+  const pad_tensor *k_weight;
+  float eps;
+  const pad_tensor *q;
+  const pad_tensor *q_weight;
+  pad_tensor *q_out;
+  float k_scale;
+  float v_scale;
+} pad_append_options;
+
+/*
+ * pad_append_kv -- puts tokens into the paged cache that pad_decode reads, with
+ * K's norm and position rotation on the way (and, as an option, the tokens'
+ * query rows beside them): everything between the projections and the
+ * attention, in one launch.  The source pages have no counterpart.
+ *
+ *  k, v          bf16 [T, Hkv, D], last dim contiguous, rows 16-byte aligned.
+ *  positions     int32 [T]: token t's place in its sequence, and the position of
+ *                its rotation.
+ *  seq_ids       int32 [T]: the sequence (row of block_tables) token t belongs to;
+ *                a negative one is padding -- nothing is written to the cache for it
+ *                (its query row is still written).  NULL: token t is sequence t's
+ *                (T = B), a decode step.
+ *  block_tables  int32 [B, max_blocks_per_seq], stride[1] == 1, as for pad_decode:
+ *                token t goes to block block_tables[seq][pos / bs], slot pos % bs.
+ *  k_cache,      bf16 or FP8 E4M3 [num_blocks, Hkv, block_size, D], the strides
+ *  v_cache       pad_decode takes; slots other than the tokens' are not touched.
+ *  options       NULL = none.
+ *
+ * No two tokens may name the same slot (two sequences sharing a page, say): which
+ * of them it then holds is not defined, and it may be parts of both.  A sequence
+ * id >= B or a block id outside [0, num_blocks) sets bit 0x1 of the device error
+ * word, a position outside the table bit 0x2 (pad_check_device_errors); the token
+ * is not written.  D in {64, 128, 256}, block_size a power of two in [1, 256].
+ * Asynchronous on `stream`, no scratch, capturable from the first call; on the
+ * same stream as the pad_decode that follows, nothing else orders the two.
+ */
+pad_status pad_append_kv(const pad_tensor *k, const pad_tensor *v, const pad_tensor *positions,
+                         const pad_tensor *seq_ids, const pad_tensor *block_tables,
+                         const pad_append_options *options, pad_tensor *k_cache, pad_tensor *v_cache,
+                         void *stream);
+
+/* Launch geometry of pad_decode_shared for one problem shape. */
+typedef struct pad_shared_plan {
+  int32_t ctas;             /* CTAs launched, one per SM */
+  int32_t chunk_tokens;     /* tokens of a step */
+  int32_t prefix_rows;      /* query rows that share one pass over the prefix */
+  int32_t prefix_blocks;    /* passes over the prefix per KV head */
+  int64_t workspace_bytes;  /* scratch */
+} pad_shared_plan;
+
+/*
+ * pad_decode_shared -- pad_decode for a batch whose sequences all begin with the
+ * same pages (a system prompt, a document): the pages are streamed once per
+ * prefix_rows query rows of a KV head instead of once per sequence, with those rows
+ * stacked into one tensor-core operand; each sequence's own tokens follow, and the
+ * two parts are merged by log-sum-exp ("perf(rocke): prepare saved paged decode
+ * bindings once", section "Summary": split-KV attention followed by a reduce).
+ * The result is pad_decode's for the same sequences.
+ *
+ *  shared_table  int32 [n], contiguous: the pages of tokens 0 .. n * block_size - 1
+ *                of every sequence, n <= max_blocks_per_seq.  n = 0: nothing shared.
+ *  block_tables  as for pad_decode, whole rows; the first n entries of a row are
+ *                not read.
+ *  seq_lens      whole lengths, the prefix included: 0 (a padding row: out = 0, lse =
+ *                -inf or the sink) or at least n * block_size.  Any other length
+ *                sets bit 0x2 of the device error word; one above the table's
+ *                capacity is clamped to it, one below n * block_size counts as 0.
+ *  options       NULL, or sinks, k_scale and v_scale as for pad_decode_ex;
+ *                window_left must be 0 (PAD_ERR_UNSUPPORTED).
+ *  workspace     NULL: the library's, one per (device, stream), grown outside
+ *                stream capture only, as for pad_decode; two graphs captured on one
+ *                stream share it and must not run at the same time.  Otherwise
+ *                256-byte aligned device memory of at least
+ *                pad_decode_shared_plan(...).workspace_bytes bytes, any contents, used
+ *                by no other call that may run at the same time.
+ * All else as for pad_decode, its envelope included.
+ */
+pad_status pad_decode_shared(const pad_tensor *q, const pad_tensor *k_cache, const pad_tensor *v_cache,
+                             const pad_tensor *shared_table, const pad_tensor *block_tables,
+                             const pad_tensor *seq_lens, float scale, const pad_decode_options *options,
+                             pad_tensor *out, pad_tensor *lse, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/*
+ * pad_decode_shared_plan -- the geometry and scratch of pad_decode_shared for a
+ * shape (shared_blocks: n), as pad_decode_plan_ex gives pad_decode's ("perf(rocke):
+ * prepare saved paged decode bindings once", section "Summary").  Pure host
+ * computation.
+ */
+pad_status pad_decode_shared_plan(int64_t batch, int64_t num_q_heads, int64_t num_kv_heads,
+                                  int64_t head_dim, int64_t block_size, int64_t max_blocks_per_seq,
+                                  int64_t shared_blocks, int32_t kv_dtype, int32_t device,
+                                  pad_shared_plan *plan);
+
+/*
  * pad_decode_plan -- the launch geometry pad_decode would use for this shape
  * (the per-shape heuristic when num_splits == 0): the geometry a saved binding
  * of "perf(rocke): prepare saved paged decode bindings once" prepares once and

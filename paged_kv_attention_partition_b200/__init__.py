@@ -8,6 +8,8 @@ fallback, and the import fails loudly if ``libpad.so`` has not been built
 
 Functions carry the C names: ``pad_decode``, ``pad_decode_with_workspace``,
 ``pad_decode_static_scratch``, ``pad_decode_tcgen05``, ``pad_decode_plan``,
+``pad_decode_shared`` (a batch behind a shared prefix), ``pad_decode_shared_plan``,
+``pad_qk_norm_rope`` (per-head norm and rotation), ``pad_append_kv`` (tokens into the cache),
 ``pad_check_device_errors``, ``pad_inject_stage_timeout``, ``pad_last_launch``,
 ``pad_release_workspace``, ``pad_status_string``, ``pad_last_error``,
 ``pad_abi_version``.
@@ -16,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Tuple, Union
 
 import torch
@@ -58,6 +61,12 @@ class PadLaunchWitness(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("kernel", "head_dim", "heads_per_tile", "kv_dtype", "stages",
                                                   "stage_tokens", "num_splits", "partition_tokens", "ctas",
                                                   "warps", "ctas_per_sm")]
+
+
+class PadSharedPlan(ctypes.Structure):
+    """pad_shared_plan: geometry and scratch of pad_decode_shared."""
+    _fields_ = [("ctas", ctypes.c_int32), ("chunk_tokens", ctypes.c_int32), ("prefix_rows", ctypes.c_int32),
+                ("prefix_blocks", ctypes.c_int32), ("workspace_bytes", ctypes.c_int64)]
 
 
 class PadError(RuntimeError):
@@ -115,6 +124,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pad_inject_stage_timeout.restype = ctypes.c_int
     lib.pad_release_workspace.argtypes = [ctypes.c_int32]
     lib.pad_release_workspace.restype = ctypes.c_int
+    # these three take descriptors packed by _Call: addresses, not PadTensor pointers
+    V, F, I = ctypes.c_void_p, ctypes.c_float, ctypes.c_int32
+    lib.pad_qk_norm_rope.argtypes = [V, V, V, V, F, V, V, I, V, V, V]
+    lib.pad_qk_norm_rope.restype = ctypes.c_int
+    lib.pad_append_kv.argtypes = [V] * 9
+    lib.pad_append_kv.restype = ctypes.c_int
+    lib.pad_decode_shared.argtypes = [V, V, V, V, V, V, F, V, V, V, V, ctypes.c_size_t, V]
+    lib.pad_decode_shared.restype = ctypes.c_int
+    lib.pad_decode_shared_plan.argtypes = [ctypes.c_int64] * 7 + [I, I, ctypes.POINTER(PadSharedPlan)]
+    lib.pad_decode_shared_plan.restype = ctypes.c_int
     lib.pad_abi_version.argtypes = []
     lib.pad_abi_version.restype = ctypes.c_int32
     _lib = lib
@@ -298,6 +317,151 @@ def pad_decode_with_workspace(q, k_cache, v_cache, block_tables, seq_lens, scale
     _raise(st)
 
 
+# pad_tensor of a tensor of 1 to 4 dims, and the two options structs that hold
+# descriptors' addresses (C layout, native alignment).
+_PACK = [None] + [struct.Struct(f"@Pii{n}q{8 * (4 - n)}x{n}q{8 * (4 - n)}x") for n in range(1, 5)]
+_PACK_APPEND = struct.Struct("@PixxxxPfxxxxPPPff")
+_PACK_DECODE = struct.Struct("@ixxxxPff")
+
+
+class _Call:
+    """The descriptors of one call, packed into one buffer: a decode step makes
+    several such calls per layer, and a ctypes structure per tensor costs more
+    than the launch.  ``at(name, t)`` is the descriptor's address (None for None)
+    and checks that the tensor is on the call's device."""
+
+    __slots__ = ("buf", "base", "used", "dev")
+
+    def __init__(self, dev: torch.device):
+        if dev.type != "cuda":
+            raise ValueError(f"expected CUDA tensors, got one on {dev}")
+        self.buf = bytearray(1280)
+        self.base = ctypes.addressof(ctypes.c_char.from_buffer(self.buf))
+        self.used = 0
+        self.dev = dev
+
+    def at(self, name: str, t: Optional[torch.Tensor]) -> Optional[int]:
+        if t is None:
+            return None
+        if t.device != self.dev:
+            raise ValueError(f"{name} is on {t.device}, expected {self.dev}")
+        dt = _DTYPES.get(t.dtype)
+        if dt is None:
+            raise TypeError(f"{name}: unsupported dtype {t.dtype}")
+        n = t.dim()
+        if not 1 <= n <= 4:
+            raise ValueError(f"{name}: 1 to 4 dims, got {n}")
+        return self.put(_PACK[n], t.data_ptr(), dt, n, *t.shape, *t.stride())
+
+    def put(self, layout: struct.Struct, *values) -> int:
+        at = self.used
+        layout.pack_into(self.buf, at, *values)
+        self.used = at + (layout.size + 7 & ~7)
+        return self.base + at
+
+    def run(self, fn, *args):
+        if self.dev.index == torch.cuda.current_device():
+            _raise(fn(*args))
+        else:
+            with torch.cuda.device(self.dev):
+                _raise(fn(*args))
+
+
+def pad_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
+                     k_weight: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None,
+                     inv_freq: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                     q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                     stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """RMS norm of every head of q [T, Hq, D] and k [T, Hkv, D] and the position
+    rotation, in one pass (see ``pad_qk_norm_rope`` in include/pad.h).
+
+    Without a weight that tensor is not normed; without ``inv_freq`` (fp32 [R/2],
+    with ``positions`` int32 [T]) nothing is rotated; k may be None.  ``q_out`` /
+    ``k_out`` receive the rows (they may be q and k themselves).  Returns (q_out, k_out)."""
+    c = _Call(q.device)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None and k is not None:
+        k_out = torch.empty(k.shape, dtype=k.dtype, device=q.device)
+    args = (c.at("q", q), c.at("k", k), c.at("q_weight", q_weight), c.at("k_weight", k_weight), eps,
+            c.at("positions", positions), c.at("inv_freq", inv_freq), int(interleaved), c.at("q_out", q_out),
+            c.at("k_out", k_out))
+    if q.numel() > 0:  # no token: no data pointers either
+        c.run(load_library().pad_qk_norm_rope, *args, _stream_handle(stream, q.device))
+    return q_out, k_out
+
+
+def pad_append_kv(k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, block_tables: torch.Tensor,
+                  k_cache: torch.Tensor, v_cache: torch.Tensor, seq_ids: Optional[torch.Tensor] = None,
+                  inv_freq: Optional[torch.Tensor] = None, interleaved: bool = False,
+                  k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, q: Optional[torch.Tensor] = None,
+                  q_weight: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                  k_scale: float = 0.0, v_scale: float = 0.0, stream=None) -> Optional[torch.Tensor]:
+    """Put tokens k, v [T, Hkv, D] into the paged cache, K normed (``k_weight``)
+    and rotated (``inv_freq``) on the way (see ``pad_append_kv`` in include/pad.h).
+
+    ``positions`` int32 [T] is each token's place in its sequence; ``seq_ids`` int32
+    [T] its row of ``block_tables`` (negative: padding, not written; None: token t is
+    sequence t's).  ``q`` [T, Hq, D]: the tokens' query rows, normed and rotated by
+    the same launch into ``q_out``.  An E4M3 cache holds x / ``k_scale``, x /
+    ``v_scale``.  Returns q_out (None without q)."""
+    c = _Call(k.device)
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if q is None and q_out is not None:
+        raise ValueError("q_out without q")
+    at = c.at
+    args = (at("k", k), at("v", v), at("positions", positions), at("seq_ids", seq_ids),
+            at("block_tables", block_tables))
+    opts = c.put(_PACK_APPEND, at("inv_freq", inv_freq) or 0, int(interleaved), at("k_weight", k_weight) or 0, eps,
+                 at("q", q) or 0, at("q_weight", q_weight) or 0, at("q_out", q_out) or 0, k_scale, v_scale)
+    if k.numel() > 0:
+        c.run(load_library().pad_append_kv, *args, opts, at("k_cache", k_cache), at("v_cache", v_cache),
+              _stream_handle(stream, k.device))
+    return q_out
+
+
+def pad_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, shared_table: torch.Tensor,
+                      block_tables: torch.Tensor, seq_lens: torch.Tensor, scale: float,
+                      out: Optional[torch.Tensor] = None, lse: Union[None, bool, torch.Tensor] = None, stream=None,
+                      sinks: Optional[torch.Tensor] = None, k_scale: float = 0.0, v_scale: float = 0.0,
+                      workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """``pad_decode`` for a batch whose sequences all begin with the pages of
+    ``shared_table`` (int32 [n]): those are read once for the batch (see
+    ``pad_decode_shared`` in include/pad.h).  ``seq_lens`` are whole lengths, 0 or at
+    least n * block_size.  ``workspace``: a contiguous tensor of at least
+    ``pad_decode_shared_plan(...)["workspace_bytes"]`` bytes instead of the
+    library's scratch.  Returns (out, lse)."""
+    c = _Call(q.device)
+    if out is None:
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    if lse is True:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    elif lse is False:
+        lse = None
+    if workspace is not None and (workspace.device != q.device or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on q's device")
+    at = c.at
+    args = (at("q", q), at("k_cache", k_cache), at("v_cache", v_cache), at("shared_table", shared_table),
+            at("block_tables", block_tables), at("seq_lens", seq_lens), scale,
+            c.put(_PACK_DECODE, 0, at("sinks", sinks) or 0, k_scale, v_scale), at("out", out), at("lse", lse))
+    if q.numel() > 0:
+        c.run(load_library().pad_decode_shared, *args, workspace.data_ptr() if workspace is not None else None,
+              workspace.numel() * workspace.element_size() if workspace is not None else 0,
+              _stream_handle(stream, q.device))
+    return out, lse
+
+
+def pad_decode_shared_plan(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, block_size: int,
+                           max_blocks_per_seq: int, shared_blocks: int, device: int = -1, kv_dtype="bf16") -> dict:
+    """Launch geometry and scratch of ``pad_decode_shared`` for a shape (no launch)."""
+    plan = PadSharedPlan()
+    _raise(load_library().pad_decode_shared_plan(batch, num_q_heads, num_kv_heads, head_dim, block_size,
+                                                 max_blocks_per_seq, shared_blocks, _KV_DTYPES.get(kv_dtype, -1),
+                                                 device, ctypes.byref(plan)))
+    return {name: getattr(plan, name) for name, _ in plan._fields_}
+
+
 def pad_decode_plan(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, block_size: int,
                     max_blocks_per_seq: int, num_splits: int = 0, device: int = -1, kv_dtype="bf16") -> dict:
     """Launch geometry pad_decode would use for this shape (no launch);
@@ -358,4 +522,5 @@ __all__ = ["pad_decode", "pad_decode_with_workspace", "pad_decode_static_scratch
            "pad_check_device_errors", "pad_release_workspace",
            "pad_status_string", "pad_last_error", "pad_abi_version", "describe", "load_library",
            "PadError", "PadTensor", "PadPlan", "PadOptions", "PadLaunchWitness", "pad_last_launch",
-           "pad_inject_stage_timeout"]
+           "pad_inject_stage_timeout", "pad_decode_shared", "pad_decode_shared_plan", "PadSharedPlan",
+           "pad_qk_norm_rope", "pad_append_kv"]

@@ -16,7 +16,9 @@
 #include <mutex>
 #include <string>
 #include <utility>
+#include <vector>
 
+#include "pad_host.h"
 #include "pad_internal.h"
 
 namespace {
@@ -318,6 +320,15 @@ std::mutex g_ws_mu;
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;   // partials
 std::map<std::pair<int, cudaStream_t>, Workspace> g_ctl;  // control blocks
 
+// host_scratch's buffers, with whether a stream capture was given one, and the
+// captured ones that a larger buffer has replaced.
+struct Scratch {
+  Workspace ws;
+  bool captured = false;
+};
+std::map<std::pair<int, cudaStream_t>, Scratch> g_scratch;
+std::vector<std::pair<int, void *>> g_scratch_kept;
+
 pad_status get_buffer(std::map<std::pair<int, cudaStream_t>, Workspace> &pool, int device, cudaStream_t stream,
                       size_t bytes, void **out) {
   std::lock_guard<std::mutex> lock(g_ws_mu);
@@ -560,6 +571,64 @@ namespace pad {
 // pad_last_error().
 void set_last_error(const char *msg) { g_last_error = msg; }
 
+pad_status host_fail(pad_status st, const char *fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  g_last_error = buf;
+  return st;
+}
+pad_status host_cuda_fail(cudaError_t e, const char *what) { return cuda_fail(e, what); }
+pad_status host_check_tensor(const pad_tensor *t, const char *name, pad_dtype dt, int ndim) {
+  return check_tensor(t, name, dt, ndim);
+}
+pad_status host_check_rows16(const pad_tensor *t, const char *name, int64_t elem_bytes) {
+  return check_rows16(t, name, elem_bytes);
+}
+pad_status host_check_device_ptr(const void *p, int device, const char *name) {
+  return check_device_ptr(p, device, name);
+}
+int host_sm_count(int device) { return sm_count(device); }
+pad_status host_check_shape(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64_t bs, int64_t W) {
+  return check_shape(Shape{B, Hq, Hkv, D, bs, W, Hkv > 0 ? Hq / Hkv : 0, false}, 0);
+}
+TensorMapEncodeFn host_tensor_map_encoder() { return tensor_map_encoder(); }
+
+pad_status host_scratch(int device, cudaStream_t stream, size_t bytes, void **out) {
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(stream, &cs);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+  const bool capturing = cs != cudaStreamCaptureStatusNone;
+  std::lock_guard<std::mutex> lock(g_ws_mu);
+  Scratch &s = g_scratch[{device, stream}];
+  if (s.ws.bytes < bytes) {
+    if (capturing)
+      return fail(PAD_ERR_WORKSPACE,
+                  "scratch must grow to %zu bytes while the stream is being captured; run one call with this shape "
+                  "outside capture first", bytes);
+    if (s.ws.ptr != nullptr && s.captured) {
+      g_scratch_kept.push_back({device, s.ws.ptr});
+    } else if (s.ws.ptr != nullptr) {
+      // queued work on this stream may still use the old buffer
+      if ((e = cudaStreamSynchronize(stream)) != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize (scratch)");
+      cudaFree(s.ws.ptr);
+    }
+    s = Scratch{};
+    e = cudaMalloc(&s.ws.ptr, bytes);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      s.ws.ptr = nullptr;
+      return fail(PAD_ERR_WORKSPACE, "cudaMalloc(%zu) for scratch failed: %s", bytes, cudaGetErrorString(e));
+    }
+    s.ws.bytes = bytes;
+  }
+  s.captured = s.captured || capturing;
+  *out = s.ws.ptr;
+  return PAD_OK;
+}
+
 pad_status decode_with_scratch_array(const pad_tensor *q, const pad_tensor *k_cache, const pad_tensor *v_cache,
                                      const pad_tensor *block_tables, const pad_tensor *seq_lens, float scale,
                                      int32_t num_splits, pad_tensor *out, pad_tensor *lse,
@@ -786,6 +855,28 @@ pad_status pad_release_workspace(int32_t device) {
       if (it->second.ptr != nullptr) cudaFree(it->second.ptr);
       it = pool->erase(it);
     }
+  }
+  std::vector<std::pair<int, void *>> drop;
+  for (auto it = g_scratch.begin(); it != g_scratch.end();) {
+    if (device >= 0 && it->first.first != device) {
+      ++it;
+      continue;
+    }
+    if (it->second.ws.ptr != nullptr) drop.push_back({it->first.first, it->second.ws.ptr});
+    it = g_scratch.erase(it);
+  }
+  for (size_t i = 0; i < g_scratch_kept.size();) {
+    if (device >= 0 && g_scratch_kept[i].first != device) {
+      ++i;
+      continue;
+    }
+    drop.push_back(g_scratch_kept[i]);
+    g_scratch_kept.erase(g_scratch_kept.begin() + (long)i);
+  }
+  for (const auto &d : drop) {
+    if ((e = cudaSetDevice(d.first)) != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+    if ((e = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
+    cudaFree(d.second);
   }
   if ((e = cudaSetDevice(cur)) != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
   return PAD_OK;

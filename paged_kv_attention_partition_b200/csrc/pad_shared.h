@@ -1,0 +1,77 @@
+// Shared-prefix decode: launch parameters and the work schedule that the main
+// kernel and the merge both derive from the lengths.
+//
+// Work is laid on one line.  An item is a set of query rows of one KV head
+// against a token range: a prefix item is a block of sequences (their heads of
+// the group, up to kSharedRows rows) against the shared pages; a rest item is
+// one sequence against its own tokens behind the prefix.  An item costs w_item
+// + chunks * (weight of a chunk), a chunk being `chunk` tokens.  CTA i of G takes
+// the line's part [i q, (i+1) q), q = ceil(total / G): it may start and end
+// inside an item, and a cut falls on the chunk whose cost contains it.  So every
+// CTA gets the same work whatever the lengths, no unit is empty, and long
+// sequences are split as far as the GPU needs.
+//
+// A unit is (item, CTA).  Items and CTAs both only grow along the line, so
+// item + CTA numbers the units without a table, and that number places a unit's
+// partial results.  (The walk itself: pad_shared_walk.cuh.)
+#pragma once
+
+#include <cuda.h>
+#include <stdint.h>
+
+#include "pad_internal.h"
+
+namespace pad {
+
+constexpr int kTileRows = 128;  // query rows of one tensor-core tile
+
+// Query rows of a unit: two tiles, one at D = 256 (whose fp32 accumulator takes
+// half of the tensor memory).
+__host__ __device__ constexpr int shared_rows(int D) { return D == 256 ? kTileRows : 2 * kTileRows; }
+// Tokens of a chunk.
+__host__ __device__ constexpr int shared_chunk(int D) { return D == 256 ? 64 : 128; }
+// Accumulators: two tiles of rows, or one tile's even and odd chunks.
+__host__ __device__ constexpr int shared_accs(int D) { return D == 256 ? 1 : 2; }
+
+struct SharedParams {
+  CUtensorMap tmk, tmv;    // caches, boxes of one 128-byte column block x box_rows slots
+  CUtensorMap tmqp, tmqr;  // q: boxes of 64 head_dim x gt heads x nseq sequences (prefix), x 1 (rest)
+  const uint16_t *q;
+  int64_t q_sb, q_sh;
+  const void *k, *v;
+  int64_t k_sblk, k_sh, k_ss, v_sblk, v_sh, v_ss;
+  const int32_t *shared_table;
+  const int32_t *tables;
+  int64_t table_stride;
+  const int32_t *seq_lens;
+  int32_t n_shared;    // pages of the prefix
+  int32_t max_blocks;  // table width, >= n_shared
+  int32_t num_blocks;
+  int32_t B, Hq, Hkv, g;
+  int32_t HT, gt;      // head tiles of a group, heads of one (the last may have fewer)
+  int32_t nseq, nrb;   // sequences of a prefix row block, row blocks
+  int32_t bs_log2;
+  int32_t ctas;
+  int32_t w_item, w_pre1, w_pre2, w_rest;  // cost of an item; of a prefix chunk of one and two tiles, of a rest chunk
+  float scale_log2, v_scale;
+  const float *sinks;
+  uint16_t *out;
+  int64_t o_sb, o_sh;
+  float *lse;
+  int64_t lse_sb, lse_sh;
+  float *o_part;     // [part rows, D], normalised by the unit's own sum
+  float *lse_part;   // [part rows], log2 units
+  int64_t rest_row0; // first part row of the rest units
+  int32_t pre_rows, rest_rows;  // part rows of a prefix and a rest unit
+  int64_t *cum;      // [B + 1] cost of the rest items before sequence b (written by CTA 0)
+  uint32_t *err;
+};
+
+// Part rows: an accumulator each for one-tile units.
+__host__ __device__ inline int shared_part_rows(int rows, int D) {
+  return shared_accs(D) == 2 && rows <= kTileRows ? 2 * rows : rows;
+}
+
+cudaError_t launch_shared(const SharedParams &p, int D, bool kv_fp8, cudaStream_t s);
+
+}  // namespace pad

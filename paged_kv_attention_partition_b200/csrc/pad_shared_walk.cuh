@@ -1,0 +1,163 @@
+// Device side of the work line of pad_shared.h: the units of a CTA, and what the
+// merge needs to find a row's units again.
+#pragma once
+
+#include "pad_shared.h"
+
+namespace pad {
+
+struct SharedUnit {
+  int32_t rest;         // 0: prefix, 1: rest
+  int32_t kvh, ht;
+  int32_t b0, nb;       // sequences b0 .. b0 + nb - 1
+  int32_t rows;         // nb * (heads of the tile)
+  int32_t heads;        // heads of the tile
+  int32_t tok0, tok1;   // tokens, tok0 a chunk's start
+  int32_t chunks;
+  int64_t part;         // first part row
+};
+
+// A sequence's length as the kernels use it: outside [0, capacity], or shorter
+// than the prefix it claims, is an error; it counts as the nearest valid one (0
+// for a sequence shorter than the prefix).
+__device__ __forceinline__ int shared_len(const SharedParams &p, int b, bool *bad) {
+  const int cap = p.max_blocks << p.bs_log2, Lp = p.n_shared << p.bs_log2;
+  const int L = __ldg(p.seq_lens + b);
+  *bad = L < 0 || L > cap || (L > 0 && L < Lp);
+  return L > cap ? cap : L < Lp ? 0 : L;
+}
+
+// Cost of a rest item of a sequence of this length.
+template <int D>
+__device__ __forceinline__ int64_t shared_rest_cost(const SharedParams &p, int L) {
+  const int n = L - (p.n_shared << p.bs_log2);
+  return n <= 0 ? 0 : p.w_item + (int64_t)((n + shared_chunk(D) - 1) / shared_chunk(D)) * p.w_rest;
+}
+
+// The prefix part of the line: items (kvh, ht, rb), rb innermost; every row block
+// is full but the last.
+struct SharedPrefix {
+  int chunks, last_nb;
+  int64_t full, last, group, total;  // costs: a full block's item, the last one's, a (kvh, ht)'s, all
+};
+template <int D>
+__device__ __forceinline__ SharedPrefix shared_prefix(const SharedParams &p) {
+  SharedPrefix s;
+  s.chunks = ((p.n_shared << p.bs_log2) + shared_chunk(D) - 1) / shared_chunk(D);
+  s.last_nb = p.B - (p.nrb - 1) * p.nseq;
+  auto cost = [&](int nb) -> int64_t {
+    return s.chunks == 0 ? 0 : p.w_item + (int64_t)s.chunks * (nb * p.gt > kTileRows ? p.w_pre2 : p.w_pre1);
+  };
+  s.full = cost(p.nseq);
+  s.last = cost(s.last_nb);
+  s.group = (p.nrb - 1) * s.full + s.last;
+  s.total = s.group * p.Hkv * p.HT;
+  return s;
+}
+
+// First chunk of an item at or behind `at` (a cost counted from the item's start).
+__device__ __forceinline__ int shared_cut(const SharedParams &p, int64_t at, int w, int chunks) {
+  if (at <= p.w_item) return 0;
+  const int64_t c = (at - p.w_item + w - 1) / w;
+  return c > chunks ? chunks : (int)c;
+}
+
+// Calls emit(unit) for each unit of CTA `cta`, in order; all lanes of a warp
+// call it together, and emit is called by all of them with the same unit.
+// cum != null: also writes the rest items' cumulative costs.
+template <int D, class Emit>
+__device__ __forceinline__ void shared_walk(const SharedParams &p, int cta, int64_t *cum, Emit &&emit) {
+  constexpr int CT = shared_chunk(D);
+  const int lane = threadIdx.x & 31;
+  const SharedPrefix pre = shared_prefix<D>(p);
+  const int Lp = p.n_shared << p.bs_log2;
+  const int hh = p.Hkv * p.HT;
+  int64_t sum = 0;
+  for (int b = lane; b < p.B; b += 32) {
+    bool bad;
+    sum += shared_rest_cost<D>(p, shared_len(p, b, &bad)) * hh;
+    if (bad && cta == 0 && cum != nullptr) atomicOr(p.err, kErrSeqLen);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  const int64_t total = pre.total + sum;
+  const int64_t q = (total + p.ctas - 1) / p.ctas;
+  int64_t pos = cta * q;
+  const int64_t end = pos + q < total ? pos + q : total;
+
+  while (pos < end && pos < pre.total) {
+    const int grp = (int)(pos / pre.group);
+    const int64_t in = pos - grp * pre.group;
+    int rb = (int)(in / pre.full);
+    if (rb > p.nrb - 1) rb = p.nrb - 1;
+    const int64_t start = grp * pre.group + rb * pre.full;
+    const int64_t cost = rb == p.nrb - 1 ? pre.last : pre.full;
+    SharedUnit u;
+    u.rest = 0;
+    u.kvh = grp / p.HT;
+    u.ht = grp % p.HT;
+    u.b0 = rb * p.nseq;
+    u.nb = rb == p.nrb - 1 ? pre.last_nb : p.nseq;
+    u.heads = min(p.gt, p.g - u.ht * p.gt);
+    u.rows = u.nb * p.gt;
+    const int w = u.rows > kTileRows ? p.w_pre2 : p.w_pre1;
+    const int c0 = shared_cut(p, pos - start, w, pre.chunks), c1 = shared_cut(p, end - start, w, pre.chunks);
+    u.tok0 = c0 * CT;
+    u.tok1 = min(c1 * CT, Lp);
+    u.chunks = c1 - c0;
+    u.part = ((int64_t)grp * p.nrb + rb + cta) * p.pre_rows;
+    if (c1 > c0) emit(u);
+    pos = start + cost;
+  }
+  if (pos >= end && cum == nullptr) return;
+
+  int64_t base = pre.total;  // cost before this round's 32 sequences
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    bool bad;
+    const int L = b < p.B ? shared_len(p, b, &bad) : 0;
+    const int64_t item = shared_rest_cost<D>(p, L);
+    int64_t incl = item * hh;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += o;
+    }
+    const int64_t first = base + incl - item * hh;
+    if (cum != nullptr && b < p.B) {
+      cum[b] = first;
+      if (b == p.B - 1) cum[p.B] = q;  // the merge needs the CTAs' share too
+    }
+    uint32_t todo = __ballot_sync(0xffffffffu, item > 0 && first < end && first + item * hh > pos);
+    while (todo != 0) {
+      const int j = __ffs(todo) - 1;
+      todo &= todo - 1;
+      const int64_t f = __shfl_sync(0xffffffffu, first, j), it = __shfl_sync(0xffffffffu, item, j);
+      const int Lj = __shfl_sync(0xffffffffu, L, j);
+      const int chunks = (Lj - Lp + CT - 1) / CT;
+      while (pos < end && pos < f + it * hh) {
+        const int k = (int)((pos - f) / it);
+        const int64_t start = f + k * it;
+        SharedUnit u;
+        u.rest = 1;
+        u.kvh = k / p.HT;
+        u.ht = k % p.HT;
+        u.b0 = b0 + j;
+        u.nb = 1;
+        u.heads = min(p.gt, p.g - u.ht * p.gt);
+        u.rows = p.gt;
+        const int c0 = shared_cut(p, pos - start, p.w_rest, chunks), c1 = shared_cut(p, end - start, p.w_rest, chunks);
+        u.tok0 = Lp + c0 * CT;
+        u.tok1 = min(Lp + c1 * CT, Lj);
+        u.chunks = c1 - c0;
+        u.part = p.rest_row0 + (((int64_t)u.b0 * hh + k) + cta) * p.rest_rows;
+        if (c1 > c0) emit(u);
+        pos = start + it;
+      }
+    }
+    base += __shfl_sync(0xffffffffu, incl, 31);
+    if (cum == nullptr && base >= end) return;
+  }
+}
+
+}  // namespace pad
