@@ -8,9 +8,12 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "pad_device.cuh"
 #include "pad_shared.h"
 #include "pad_shared_walk.cuh"
+#include "pad_tc.cuh"
 
 namespace pad {
 namespace {
@@ -63,6 +66,401 @@ __global__ void __launch_bounds__(256) shared_kernel(const __grid_constant__ Sha
       }
     }
   });
+}
+
+// ---- the partial kernel -------------------------------------------------------
+//
+// One persistent CTA per SM, warp-specialised; every role goes through the CTA's
+// units in order, each as far ahead as its buffers let it:
+//
+//   schedule warp   walks the work line and puts units into a queue of kQueue
+//   copy warp       TMA of the unit's q rows, then of its K and V chunks into one
+//                   ring (items K0 K1 V0 K2 V1 ...), boxes of one 128-byte column
+//                   block x one page (or a chunk's worth of a larger page)
+//   MMA thread      S = Q . K^T  (128 rows x chunk) into one of two S buffers, then
+//                   O += P . V  with P read from tensor memory
+//   softmax warps   thread = row: scores out of tensor memory, running maximum and
+//                   sum, P back over the scores it was made from
+//
+// A step is (query tile, chunk): S buffer of a step = its parity, so one step's
+// softmax runs under the other's products.  A two-tile unit takes both tiles
+// through each chunk; a one-tile unit alternates its even and odd chunks between
+// the two accumulators, which leave two partials per row.  At D = 256 there is one
+// accumulator (256 of the 512 columns), one softmax group, and still two S buffers.
+//
+// The P of a step overlays its S: PV(j) is issued before QK(j + 2), and the tensor
+// core runs one thread's products in order, so a QK never overwrites a P that is
+// still to be read.
+template <int D>
+struct SharedCfg {
+  static constexpr int CT = shared_chunk(D), NACC = shared_accs(D), CB = D / 64;
+  static constexpr int QR = shared_rows(D);
+  static constexpr uint32_t kSlot = CT * D * 2;         // bytes of a K or V chunk
+  static constexpr uint32_t kBlock = CT * 128;          // one column block of it
+  static constexpr uint32_t kQBlock = QR * 128;         // one column block of q
+  static constexpr uint32_t kQ = CB * kQBlock;
+  static constexpr int NS = D == 64 ? 8 : 5;            // ring slots
+  static constexpr int kQueue = 4;
+  static constexpr int kSoftmaxWarps = 4 * NACC;
+  static constexpr int kCopyWarp = kSoftmaxWarps, kMmaWarp = kSoftmaxWarps + 1, kScheduleWarp = kSoftmaxWarps + 2;
+  static constexpr int kThreads = (kSoftmaxWarps + 3) * 32;
+  static constexpr uint32_t ring = kQ, queue = ring + NS * kSlot, bars = queue + kQueue * 64;
+  static constexpr uint32_t total = bars + 512 + 1024 /* alignment slack */;
+  static constexpr uint32_t kSCol = 128, kOCol = 256;   // S buffers at 0 and 128, O behind them
+};
+static_assert(sizeof(SharedUnit) <= 64, "queue entry");
+
+template <int D>
+__global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(const __grid_constant__ SharedParams p) {
+  using C = SharedCfg<D>;
+  constexpr int CT = C::CT, NACC = C::NACC, NS = C::NS, CB = C::CB;
+  static_assert(C::total <= (uint32_t)kSmemBudget, "shared-memory plan over budget");
+  static_assert(C::kOCol + NACC * D <= 512, "tensor memory");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sq = smem_addr(smem), sring = sq + C::ring;
+  SharedUnit *queue = reinterpret_cast<SharedUnit *>(smem + C::queue);  // entries 64 bytes apart
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::bars);
+  const uint32_t bar0 = smem_addr(bars);
+  const uint32_t full = bar0, empty = full + 8 * NS, q_full = empty + 8 * NS, q_empty = q_full + 16,
+                 s_full = q_empty + 16, p_full = s_full + 16, pv_done = p_full + 16, o_free = pv_done + 16,
+                 u_full = o_free + 16, u_empty = u_full + 8 * C::kQueue, idle = u_empty + 8 * C::kQueue;
+  constexpr int kBars = 2 * NS + 12 + 2 * C::kQueue + 1;
+  static_assert(kBars * 8 + 16 <= 512, "barrier area");
+  uint32_t *words = reinterpret_cast<uint32_t *>(bars + kBars);  // [0] tmem, [1] abort
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(words + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(q_full + 8 * i, 1);
+      mbar_init(q_empty + 8 * i, 1);
+      mbar_init(s_full + 8 * i, 1);
+      mbar_init(p_full + 8 * i, 4);   // a softmax group's warps
+      mbar_init(pv_done + 8 * i, 1);
+      mbar_init(o_free + 8 * i, 4);
+    }
+    for (int i = 0; i < C::kQueue; ++i) {
+      mbar_init(u_full + 8 * i, 1);
+      mbar_init(u_empty + 8 * i, C::kSoftmaxWarps + 2);  // every role's warps
+    }
+    mbar_init(idle, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tc::alloc(smem_addr(words), 512);
+    tc::relinquish();
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = words[0];
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // the merge may come up as CTAs end
+
+  auto wait = [&](uint32_t bar, uint32_t parity, bool drain = false) {
+    return tc::wait(bar, parity, p.err, abort_flag, drain);
+  };
+  // Unit k of the queue, by a whole warp; false: give up.  chunks == 0 ends.
+  auto next_unit = [&](int k, SharedUnit &u) -> bool {
+    const int e = k % C::kQueue;
+    if (!__all_sync(0xffffffffu, wait(u_full + 8 * e, (k / C::kQueue) & 1))) return false;
+    u = *reinterpret_cast<const SharedUnit *>(reinterpret_cast<const uint8_t *>(queue) + 64 * e);
+    __syncwarp();
+    if (lane == 0) tc::arrive(u_empty + 8 * e);
+    return true;
+  };
+  // Half of the q buffer a unit's rows take: both when its box has more than 128
+  // rows, else each half in turn (one at D = 256).
+  auto q_box_rows = [&](const SharedUnit &u) { return p.gt * (u.rest ? 1 : p.nseq); };
+
+  if (warp == C::kScheduleWarp) {
+    int k = 0;
+    bool ok = true;
+    auto put = [&](const SharedUnit &u) {
+      const int e = k % C::kQueue;
+      ok = ok && (k < C::kQueue || __all_sync(0xffffffffu, wait(u_empty + 8 * e, (k / C::kQueue - 1) & 1)));
+      if (ok && lane == 0) {
+        *reinterpret_cast<SharedUnit *>(reinterpret_cast<uint8_t *>(queue) + 64 * e) = u;
+        tc::arrive(u_full + 8 * e);
+      }
+      ++k;
+    };
+    shared_walk<D>(p, blockIdx.x, blockIdx.x == 0 ? p.cum : nullptr, put);
+    SharedUnit end{};
+    put(end);
+  } else if (warp == C::kCopyWarp) {
+    const int box_log2 = min(p.bs_log2, CT == 128 ? 7 : 6);
+    const int nbox = CT >> box_log2, copies = nbox * CB;
+    uint32_t item = 0;               // ring items issued
+    uint32_t qn[2] = {0, 0};         // uses of each half
+    int half = 0;
+    bool ok = true;
+    SharedUnit u;
+    for (int k = 0; ok && (ok = next_unit(k, u)) && u.chunks > 0; ++k) {
+      // ---- q
+      const int box_rows = q_box_rows(u);
+      const bool both = NACC == 2 && box_rows > kTileRows;
+      const int h = both || NACC == 1 ? 0 : half;
+      if (!both && NACC == 2) half ^= 1;
+      ok = qn[h] == 0 || __all_sync(0xffffffffu, wait(q_empty + 8 * h, (qn[h] - 1) & 1));
+      if (both) ok = ok && (qn[1] == 0 || __all_sync(0xffffffffu, wait(q_empty + 8, (qn[1] - 1) & 1)));
+      if (!ok) break;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(q_full + 8 * h, (uint32_t)box_rows * 128 * CB);
+        if (both) tc::arrive(q_full + 8);
+        for (int cb = 0; cb < CB; ++cb)
+          tma_load_4d(sq + cb * C::kQBlock + h * (kTileRows * 128), u.rest ? &p.tmqr : &p.tmqp, 0,
+                      u.kvh * p.g + u.ht * p.gt, cb, u.b0, q_full + 8 * h);
+      }
+      ++qn[h];
+      if (both) ++qn[1];
+      // ---- K and V chunks
+      const int32_t *table = u.rest ? p.tables + u.b0 * p.table_stride : p.shared_table;
+      auto copy = [&](const CUtensorMap *map, int c, bool rows1) -> bool {
+        const int slot = item % NS;
+        if (item >= NS && !__all_sync(0xffffffffu, wait(empty + 8 * slot, (item / NS - 1) & 1))) return false;
+        const uint32_t bar = full + 8 * slot, dst = sring + slot * C::kSlot;
+        if (lane == 0) mbar_arrive_expect_tx(bar, C::kSlot);
+        __syncwarp();
+        const int tb = u.tok0 + c * CT;
+        // block of the page that holds token t; num_blocks (reads as zeros) behind the
+        // unit's tokens and for an id that is not one
+        auto block_of = [&](int t) -> int {
+          if (t >= u.tok1) return p.num_blocks;
+          const int id = __ldg(table + (t >> p.bs_log2));
+          if ((unsigned)id < (unsigned)p.num_blocks) return id;
+          atomicOr(p.err, kErrBlockId);
+          return p.num_blocks;
+        };
+        const int slot_mask = (1 << p.bs_log2) - 1, box = 1 << box_log2;
+        // V's box that a sequence ends in: row by row, so that the slots behind the
+        // sequence are zeros, whatever they hold (a weight of 0 times NaN is NaN)
+        const int part = rows1 && u.tok1 < tb + CT && (u.tok1 & (box - 1)) != 0 ? (u.tok1 - tb) >> box_log2 : -1;
+        for (int x = lane; x < copies; x += 32) {
+          const int j = x & (nbox - 1), cb = x / nbox, t = tb + (j << box_log2);
+          if (j != part)
+            tma_load_5d(dst + cb * C::kBlock + ((uint32_t)j << (box_log2 + 7)), map, 0, t & slot_mask, cb, u.kvh,
+                        block_of(t), bar);
+        }
+        if (part >= 0) {
+          for (int x = lane; x < box * CB; x += 32) {
+            const int i = (part << box_log2) + (x & (box - 1)), cb = x >> box_log2;
+            tma_load_5d(dst + cb * C::kBlock + i * 128, &p.tmv1, 0, (tb + i) & slot_mask, cb, u.kvh, block_of(tb + i),
+                        bar);
+          }
+        }
+        ++item;
+        return true;
+      };
+      ok = copy(&p.tmk, 0, false);
+      for (int c = 0; ok && c < u.chunks; ++c) {
+        if (c + 1 < u.chunks) ok = copy(&p.tmk, c + 1, false);
+        ok = ok && copy(&p.tmv, c, true);
+      }
+    }
+    if (lane == 0) {  // leave no copy in flight, whoever gives up
+      for (uint32_t i = item > NS ? item - NS : 0; i < item; ++i) wait(full + 8 * (i % NS), (i / NS) & 1, true);
+      for (int h = 0; h < 2; ++h)
+        if (qn[h] > 0) wait(q_full + 8 * h, (qn[h] - 1) & 1, true);
+    }
+  } else if (warp == C::kMmaWarp) {
+    constexpr uint32_t IQK = tc::idesc(CT, false, false), IPV = tc::idesc(D, true, false);
+    uint32_t item = 0, step = 0, qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0};
+    int half = 0;
+    bool ok = true;
+    SharedUnit u;
+    for (int k = 0; ok && (ok = next_unit(k, u)) && u.chunks > 0; ++k) {
+      const bool two = NACC == 2 && u.rows > kTileRows;
+      const bool both = NACC == 2 && q_box_rows(u) > kTileRows;
+      const int h = both || NACC == 1 ? 0 : half;
+      if (!both && NACC == 2) half ^= 1;
+      const int steps = two ? 2 * u.chunks : u.chunks;
+      if (lane == 0) {
+        auto k_item = [&](int c) { return item + (c == 0 ? 0 : 2 * c - 1); };
+        auto v_item = [&](int c) { return item + (c == u.chunks - 1 ? 2 * c + 1 : 2 * c + 2); };
+        auto qk = [&](int j) -> bool {
+          const int c = two ? j >> 1 : j, tile = two ? j & 1 : 0, buf = (step + j) & 1;
+          const uint32_t it = k_item(c), slot = it % NS;
+          if (!wait(full + 8 * slot, (it / NS) & 1)) return false;
+          tc::fence_after();
+          const uint32_t qb = sq + (h + tile) * (kTileRows * 128), kb = sring + slot * C::kSlot;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::mma_ss(tmem + buf * C::kSCol, tc::smem_desc(qb + (kk >> 2) * C::kQBlock + (kk & 3) * 32, 16, 1024),
+                       tc::smem_desc(kb + (kk >> 2) * C::kBlock + (kk & 3) * 32, 16, 1024), IQK, kk > 0);
+          tc::commit(s_full + 8 * buf);
+          if (!two || tile == 1) tc::commit(empty + 8 * slot);
+          if (j == steps - 1) {
+            tc::commit(q_empty + 8 * h);
+            if (both) tc::commit(q_empty + 8);
+          }
+          return true;
+        };
+        auto pv = [&](int j) -> bool {
+          const int c = two ? j >> 1 : j, buf = (step + j) & 1, acc = NACC == 2 ? buf : 0;
+          const bool first = j < NACC;
+          const uint32_t it = v_item(c), slot = it % NS;
+          if (!wait(p_full + 8 * buf, pn[buf] & 1)) return false;
+          ++pn[buf];
+          if (!wait(full + 8 * slot, (it / NS) & 1)) return false;
+          if (first) {  // the last unit's sums have been read
+            if (on[acc] > 0 && !wait(o_free + 8 * acc, (on[acc] - 1) & 1)) return false;
+            ++on[acc];
+          }
+          tc::fence_after();
+          const uint32_t vb = sring + slot * C::kSlot;
+#pragma unroll
+          for (int kk = 0; kk < CT / 16; ++kk)
+            tc::mma_ts(tmem + C::kOCol + acc * D, tmem + buf * C::kSCol + kk * 8,
+                       tc::smem_desc(vb + kk * 2048, C::kBlock, 1024), IPV, !first || kk > 0);
+          tc::commit(pv_done + 8 * acc);
+          if (!two || (j & 1)) tc::commit(empty + 8 * slot);
+          return true;
+        };
+        ok = wait(q_full + 8 * h, qn[h] & 1) && (!both || wait(q_full + 8, qn[1] & 1));
+        ok = ok && qk(0) && (steps < 2 || qk(1));
+        for (int j = 0; ok && j < steps; ++j) ok = pv(j) && (j + 2 >= steps || qk(j + 2));
+      }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+      ++qn[h];
+      if (both) ++qn[1];
+      item += 2 * u.chunks;
+      step += steps;
+    }
+    if (lane == 0) tc::commit(idle);  // every product issued above has completed when this arrives
+  } else {
+    // ---- softmax: thread = row of the group's tile
+    const int w = warp >> 2, wq = warp & 3, row_in_tile = wq * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
+    const float sl2 = p.scale_log2;
+    uint32_t step = 0;               // steps of all units so far
+    uint32_t sn[2] = {0, 0};         // S buffer uses
+    uint32_t vn = 0;                 // products into this group's accumulator
+    bool ok = true;
+    SharedUnit u;
+    for (int k = 0; ok && (ok = next_unit(k, u)) && u.chunks > 0; ++k) {
+      const bool two = NACC == 2 && u.rows > kTileRows;
+      const int steps = two ? 2 * u.chunks : u.chunks;
+      const int j0 = NACC == 2 ? (w ^ (int)step) & 1 : 0;  // the unit's first step of this group
+      const int tile = two ? j0 : 0;
+      const int r = tile * kTileRows + row_in_tile;
+      const bool live = tile * kTileRows + wq * 32 < u.rows;  // the warp has a row
+      const uint32_t ocol = lanes + C::kOCol + (NACC == 2 ? w : 0) * D;
+      float m = -INFINITY, l = 0.f;
+      for (int j = j0; ok && j < steps; j += NACC) {
+        const int buf = (int)(step + j) & 1;
+        ok = __all_sync(0xffffffffu, wait(s_full + 8 * buf, sn[buf] & 1));
+        ++sn[buf];
+        if (!ok) break;
+        if (live) {
+          tc::fence_after();
+          const uint32_t scol = lanes + buf * C::kSCol;
+          float s[CT];
+#pragma unroll
+          for (int i = 0; i < CT; i += 32) tc::ld32(scol + i, s + i);
+          tc::wait_ld();
+          const int nv = u.tok1 - (u.tok0 + (two ? j >> 1 : j) * CT);
+          if (nv < CT) {  // the last chunk's tokens behind the range
+#pragma unroll
+            for (int i = 0; i < CT; ++i)
+              if (i >= nv) s[i] = sl2 >= 0.f ? -INFINITY : INFINITY;
+          }
+          float mx[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[i] = sl2 >= 0.f ? -INFINITY : INFINITY;
+          if (sl2 >= 0.f) {
+#pragma unroll
+            for (int i = 0; i < CT; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
+            mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < CT; ++i) mx[i & 3] = fminf(mx[i & 3], s[i]);
+            mx[0] = fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3]));
+          }
+          const float top = mx[0] * sl2;
+          // The reference moves only when a score passes it by 2^8: any
+          // reference gives the same result as long as l and O share it, and the
+          // rescale of O is skipped on almost every chunk.
+          if (__any_sync(0xffffffffu, top > m + 8.f)) {
+            const float mn = fmaxf(m, top);
+            const float a = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
+            m = mn;
+            l *= a;
+            if (j != j0) {  // O holds the earlier chunks once their product is done
+              ok = __all_sync(0xffffffffu, wait(pv_done + 8 * (NACC == 2 ? w : 0), (vn - 1) & 1));
+              if (!ok) break;
+              tc::fence_after();
+#pragma unroll
+              for (int i = 0; i < D; i += 32) {
+                float o[32];
+                tc::ld32(ocol + i, o);
+                tc::wait_ld();
+#pragma unroll
+                for (int x = 0; x < 32; ++x) o[x] *= a;
+                tc::st32(ocol + i, reinterpret_cast<const uint32_t *>(o));
+              }
+            }
+          }
+          const float ref = m == -INFINITY ? 0.f : m;
+          uint32_t pk[CT / 2];
+          float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < CT; i += 2) {
+            const float e0 = fast_exp2(s[i] * sl2 - ref), e1 = fast_exp2(s[i + 1] * sl2 - ref);
+            ls[i & 2] += e0;
+            ls[(i & 2) + 1] += e1;
+            pk[i / 2] = pack_bf16x2(e0, e1);
+          }
+          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);  // fp32 weights: rounded ones would move lse by up to 2^-9
+#pragma unroll
+          for (int i = 0; i < CT / 2; i += 32) tc::st32(scol + i, pk + i);
+          tc::wait_st();
+          tc::fence_before();
+        }
+        ++vn;
+        __syncwarp();
+        if (lane == 0) tc::arrive(p_full + 8 * buf);
+      }
+      if (ok && steps > j0) {
+        ok = __all_sync(0xffffffffu, wait(pv_done + 8 * (NACC == 2 ? w : 0), (vn - 1) & 1));
+        if (ok && live) {
+          tc::fence_after();
+          const float inv = 1.f / l;
+          const int64_t row = u.part + (two || NACC == 1 ? 0 : (int64_t)j0 * u.rows) + r;
+          float4 *dst = reinterpret_cast<float4 *>(p.o_part + row * D);
+#pragma unroll
+          for (int i = 0; i < D; i += 32) {
+            float o[32];
+            tc::ld32(ocol + i, o);
+            tc::wait_ld();
+            if (r < u.rows) {
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                dst[i / 4 + x] = make_float4(o[4 * x] * inv, o[4 * x + 1] * inv, o[4 * x + 2] * inv, o[4 * x + 3] * inv);
+            }
+          }
+          if (r < u.rows) p.lse_part[row] = m + log2f(l);
+          tc::fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) tc::arrive(o_free + 8 * (NACC == 2 ? w : 0));
+      }
+      step += steps;
+    }
+  }
+
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    wait(idle, 0, true);  // no product may write tensor memory that is given back
+    tc::fence_after();
+    tc::dealloc(tmem, 512);
+  }
 }
 
 // One warp per query row: the row's prefix units and rest units, found again
@@ -131,9 +529,23 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const __grid_constant
 
 template <int D, bool F8>
 cudaError_t launch_t(const SharedParams &p, cudaStream_t s) {
-  shared_kernel<D, F8><<<p.ctas, 256, 0, s>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
+  if constexpr (F8) {
+    shared_kernel<D, F8><<<p.ctas, 256, 0, s>>>(p);
+  } else {
+    static std::atomic<uint64_t> attr_done{0};
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(attr_done.load(std::memory_order_acquire) & bit)) {
+      e = cudaFuncSetAttribute(shared_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)SharedCfg<D>::total);
+      if (e != cudaSuccess) return e;
+      attr_done.fetch_or(bit, std::memory_order_acq_rel);
+    }
+    shared_tc_kernel<D><<<p.ctas, SharedCfg<D>::kThreads, SharedCfg<D>::total, s>>>(p);
+  }
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int64_t rows = (int64_t)p.B * p.Hq;
   shared_merge_kernel<D><<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(p);
   return cudaGetLastError();

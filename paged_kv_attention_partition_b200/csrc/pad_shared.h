@@ -34,7 +34,8 @@ __host__ __device__ constexpr int shared_chunk(int D) { return D == 256 ? 64 : 1
 __host__ __device__ constexpr int shared_accs(int D) { return D == 256 ? 1 : 2; }
 
 struct SharedParams {
-  CUtensorMap tmk, tmv;    // caches, boxes of one 128-byte column block x box_rows slots
+  CUtensorMap tmk, tmv;    // caches, boxes of one 128-byte column block x a page (at most a chunk)
+  CUtensorMap tmv1;        // V with boxes of one slot
   CUtensorMap tmqp, tmqr;  // q: boxes of 64 head_dim x gt heads x nseq sequences (prefix), x 1 (rest)
   const uint16_t *q;
   int64_t q_sb, q_sh;

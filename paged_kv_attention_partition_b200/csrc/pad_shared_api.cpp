@@ -248,6 +248,7 @@ extern "C" pad_status pad_decode_shared(const pad_tensor *q, const pad_tensor *k
   const int box = (int)(bs < pad::shared_chunk((int)D) ? bs : pad::shared_chunk((int)D));
   if ((st = cache_map(&p.tmk, k_cache, box, "k_cache")) != PAD_OK) return st;
   if ((st = cache_map(&p.tmv, v_cache, box, "v_cache")) != PAD_OK) return st;
+  if ((st = cache_map(&p.tmv1, v_cache, 1, "v_cache")) != PAD_OK) return st;
   if ((st = query_map(&p.tmqp, q, p.gt, p.nseq)) != PAD_OK) return st;
   if ((st = query_map(&p.tmqr, q, p.gt, 1)) != PAD_OK) return st;
   p.q = static_cast<const uint16_t *>(q->data);
@@ -267,6 +268,9 @@ extern "C" pad_status pad_decode_shared(const pad_tensor *q, const pad_tensor *k
   p.seq_lens = static_cast<const int32_t *>(seq_lens->data);
   p.num_blocks = (int32_t)NB;
   p.scale_log2 = (float)((double)scale * (double)k_scale * 1.4426950408889634);
+  // a scale of 0 weighs every token alike; the smallest positive one does too, and
+  // keeps a masked score, -inf, at -inf
+  if (p.scale_log2 == 0.f) p.scale_log2 = 1.4e-45f;
   p.v_scale = v_scale;
   p.sinks = sinks != nullptr ? static_cast<const float *>(sinks->data) : nullptr;
   p.out = static_cast<uint16_t *>(out->data);
