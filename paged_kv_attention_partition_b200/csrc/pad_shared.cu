@@ -74,10 +74,10 @@ __global__ void __launch_bounds__(256) shared_kernel(const __grid_constant__ Sha
 // units in order, each as far ahead as its buffers let it:
 //
 //   schedule warp   walks the work line and puts units into a queue of kQueue
-//   copy warp       TMA of the unit's q rows, then of its K and V chunks into one
-//                   ring (items K0 K1 V0 K2 V1 ...), boxes of one 128-byte column
+//   copy warps      TMA of the unit's q rows and K chunks, and of its V chunks, into
+//                   one ring (items K0 K1 V0 K2 V1 ...), boxes of one 128-byte column
 //                   block x one page (or a chunk's worth of a larger page)
-//   MMA thread      S = Q . K^T  (128 rows x chunk) into one of two S buffers, then
+//   MMA warp        S = Q . K^T  (128 rows x chunk) into one of two S buffers, then
 //                   O += P . V  with P read from tensor memory
 //   softmax warps   thread = row: scores out of tensor memory, running maximum and
 //                   sum, P back over the scores it was made from
@@ -102,8 +102,9 @@ struct SharedCfg {
   static constexpr int NS = D == 64 ? 8 : 5;            // ring slots
   static constexpr int kQueue = 4;
   static constexpr int kSoftmaxWarps = 4 * NACC;
-  static constexpr int kCopyWarp = kSoftmaxWarps, kMmaWarp = kSoftmaxWarps + 1, kScheduleWarp = kSoftmaxWarps + 2;
-  static constexpr int kThreads = (kSoftmaxWarps + 3) * 32;
+  static constexpr int kCopyKWarp = kSoftmaxWarps, kCopyVWarp = kSoftmaxWarps + 1, kMmaWarp = kSoftmaxWarps + 2,
+                       kScheduleWarp = kSoftmaxWarps + 3;
+  static constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
   static constexpr uint32_t ring = kQ, queue = ring + NS * kSlot, bars = queue + kQueue * 64;
   static constexpr uint32_t total = bars + 512 + 1024 /* alignment slack */;
   static constexpr uint32_t kSCol = 128, kOCol = 256;   // S buffers at 0 and 128, O behind them
@@ -126,15 +127,17 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
                  s_full = q_empty + 16, p_full = s_full + 16, pv_done = p_full + 16, o_free = pv_done + 16,
                  u_full = o_free + 16, u_empty = u_full + 8 * C::kQueue, idle = u_empty + 8 * C::kQueue;
   constexpr int kBars = 2 * NS + 12 + 2 * C::kQueue + 1;
-  static_assert(kBars * 8 + 16 <= 512, "barrier area");
+  static_assert(kBars * 8 + 8 + 8 * NS <= 512, "barrier area");
   uint32_t *words = reinterpret_cast<uint32_t *>(bars + kBars);  // [0] tmem, [1] abort
   volatile int *abort_flag = reinterpret_cast<volatile int *>(words + 1);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint32_t *filled = words + 2;  // [NS][2] 1 + the last item that each copy warp put into a slot
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 1);
+      filled[2 * i] = filled[2 * i + 1] = 0;
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + 8 * i, 1);
@@ -146,7 +149,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
     }
     for (int i = 0; i < C::kQueue; ++i) {
       mbar_init(u_full + 8 * i, 1);
-      mbar_init(u_empty + 8 * i, C::kSoftmaxWarps + 2);  // every role's warps
+      mbar_init(u_empty + 8 * i, C::kSoftmaxWarps + 3);  // every role's warps
     }
     mbar_init(idle, 1);
     *abort_flag = 0;
@@ -159,7 +162,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
   tc::fence_before();
   __syncthreads();
   tc::fence_after();
-  const uint32_t tmem = words[0];
+  const uint32_t tmem = __shfl_sync(0xffffffffu, words[0], 0);
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // the merge may come up as CTAs end
 
   auto wait = [&](uint32_t bar, uint32_t parity, bool drain = false) {
@@ -193,86 +196,104 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
     shared_walk<D>(p, blockIdx.x, blockIdx.x == 0 ? p.cum : nullptr, put);
     SharedUnit end{};
     put(end);
-  } else if (warp == C::kCopyWarp) {
-    const int box_log2 = min(p.bs_log2, CT == 128 ? 7 : 6);
-    const int nbox = CT >> box_log2, copies = nbox * CB;
-    uint32_t item = 0;               // ring items issued
-    uint32_t qn[2] = {0, 0};         // uses of each half
+  } else if (warp == C::kCopyKWarp || warp == C::kCopyVWarp) {
+    const bool is_k = warp == C::kCopyKWarp;
+    const CUtensorMap *map = is_k ? &p.tmk : &p.tmv;
+    const int box_log2 = min(p.bs_log2, CT == 128 ? 7 : 6), box = 1 << box_log2, nbox = CT >> box_log2;
+    const int slot_mask = (1 << p.bs_log2) - 1;
+    uint32_t base = 0;               // ring items of the units before this one
+    uint32_t qn[2] = {0, 0};         // uses of each half of q
     int half = 0;
     bool ok = true;
     SharedUnit u;
     for (int k = 0; ok && (ok = next_unit(k, u)) && u.chunks > 0; ++k) {
-      // ---- q
-      const int box_rows = q_box_rows(u);
-      const bool both = NACC == 2 && box_rows > kTileRows;
-      const int h = both || NACC == 1 ? 0 : half;
-      if (!both && NACC == 2) half ^= 1;
-      ok = qn[h] == 0 || __all_sync(0xffffffffu, wait(q_empty + 8 * h, (qn[h] - 1) & 1));
-      if (both) ok = ok && (qn[1] == 0 || __all_sync(0xffffffffu, wait(q_empty + 8, (qn[1] - 1) & 1)));
-      if (!ok) break;
-      if (lane == 0) {
-        mbar_arrive_expect_tx(q_full + 8 * h, (uint32_t)box_rows * 128 * CB);
-        if (both) tc::arrive(q_full + 8);
-        for (int cb = 0; cb < CB; ++cb)
-          tma_load_4d(sq + cb * C::kQBlock + h * (kTileRows * 128), u.rest ? &p.tmqr : &p.tmqp, 0,
-                      u.kvh * p.g + u.ht * p.gt, cb, u.b0, q_full + 8 * h);
-      }
-      ++qn[h];
-      if (both) ++qn[1];
-      // ---- K and V chunks
       const int32_t *table = u.rest ? p.tables + u.b0 * p.table_stride : p.shared_table;
-      auto copy = [&](const CUtensorMap *map, int c, bool rows1) -> bool {
-        const int slot = item % NS;
-        if (item >= NS && !__all_sync(0xffffffffu, wait(empty + 8 * slot, (item / NS - 1) & 1))) return false;
-        const uint32_t bar = full + 8 * slot, dst = sring + slot * C::kSlot;
-        if (lane == 0) mbar_arrive_expect_tx(bar, C::kSlot);
-        __syncwarp();
-        const int tb = u.tok0 + c * CT;
-        // block of the page that holds token t; num_blocks (reads as zeros) behind the
-        // unit's tokens and for an id that is not one
-        auto block_of = [&](int t) -> int {
-          if (t >= u.tok1) return p.num_blocks;
-          const int id = __ldg(table + (t >> p.bs_log2));
-          if ((unsigned)id < (unsigned)p.num_blocks) return id;
-          atomicOr(p.err, kErrBlockId);
-          return p.num_blocks;
-        };
-        const int slot_mask = (1 << p.bs_log2) - 1, box = 1 << box_log2;
-        // V's box that a sequence ends in: row by row, so that the slots behind the
-        // sequence are zeros, whatever they hold (a weight of 0 times NaN is NaN)
-        const int part = rows1 && u.tok1 < tb + CT && (u.tok1 & (box - 1)) != 0 ? (u.tok1 - tb) >> box_log2 : -1;
-        for (int x = lane; x < copies; x += 32) {
-          const int j = x & (nbox - 1), cb = x / nbox, t = tb + (j << box_log2);
-          if (j != part)
-            tma_load_5d(dst + cb * C::kBlock + ((uint32_t)j << (box_log2 + 7)), map, 0, t & slot_mask, cb, u.kvh,
-                        block_of(t), bar);
-        }
-        if (part >= 0) {
-          for (int x = lane; x < box * CB; x += 32) {
-            const int i = (part << box_log2) + (x & (box - 1)), cb = x >> box_log2;
-            tma_load_5d(dst + cb * C::kBlock + i * 128, &p.tmv1, 0, (tb + i) & slot_mask, cb, u.kvh, block_of(tb + i),
-                        bar);
+      // Block of each box of a chunk, box j's in lane j % 32: num_blocks (reads as
+      // zeros) behind the unit's tokens and for an id that is not one.  Fetched a
+      // chunk ahead, so that the table's latency is not in the copies' way.
+      int ids[CT / 32];
+      auto fetch = [&](int c) {
+#pragma unroll
+        for (int w = 0; w < CT / 32; ++w) {
+          const int t = u.tok0 + c * CT + ((32 * w + lane) << box_log2);
+          ids[w] = p.num_blocks;
+          if (32 * w < nbox && 32 * w + lane < nbox && t < u.tok1) {
+            const int id = __ldg(table + (t >> p.bs_log2));
+            if ((unsigned)id < (unsigned)p.num_blocks) ids[w] = id;
+            else atomicOr(p.err, kErrBlockId);
           }
         }
-        ++item;
-        return true;
       };
-      ok = copy(&p.tmk, 0, false);
-      for (int c = 0; ok && c < u.chunks; ++c) {
-        if (c + 1 < u.chunks) ok = copy(&p.tmk, c + 1, false);
-        ok = ok && copy(&p.tmv, c, true);
+      fetch(0);
+      if (is_k) {  // ---- q
+        const int box_rows = q_box_rows(u);
+        const bool both = NACC == 2 && box_rows > kTileRows;
+        const int h = both || NACC == 1 ? 0 : half;
+        if (!both && NACC == 2) half ^= 1;
+        ok = qn[h] == 0 || __all_sync(0xffffffffu, wait(q_empty + 8 * h, (qn[h] - 1) & 1));
+        if (both) ok = ok && (qn[1] == 0 || __all_sync(0xffffffffu, wait(q_empty + 8, (qn[1] - 1) & 1)));
+        if (!ok) break;
+        if (tc::elect()) {
+          mbar_arrive_expect_tx(q_full + 8 * h, (uint32_t)box_rows * 128 * CB);
+          if (both) tc::arrive(q_full + 8);
+          for (int cb = 0; cb < CB; ++cb)
+            tma_load_4d(sq + cb * C::kQBlock + h * (kTileRows * 128), u.rest ? &p.tmqr : &p.tmqp, 0,
+                        u.kvh * p.g + u.ht * p.gt, cb, u.b0, q_full + 8 * h);
+        }
+        __syncwarp();
+        ++qn[h];
+        if (both) ++qn[1];
       }
+      // ---- this warp's chunks
+      for (int c = 0; ok && c < u.chunks; ++c) {
+        const uint32_t item = base + (is_k ? (c == 0 ? 0 : 2 * c - 1) : c == u.chunks - 1 ? 2 * c + 1 : 2 * c + 2);
+        const int slot = item % NS;
+        if (item >= NS && !__all_sync(0xffffffffu, wait(empty + 8 * slot, (item / NS - 1) & 1))) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = full + 8 * slot, dst = sring + slot * C::kSlot;
+        const int tb = u.tok0 + c * CT;
+        // V's box that a sequence ends in: row by row, so that the slots behind the
+        // sequence are zeros, whatever they hold (a weight of 0 times NaN is NaN)
+        const int part = !is_k && u.tok1 < tb + CT && (u.tok1 & (box - 1)) != 0 ? (u.tok1 - tb) >> box_log2 : -1;
+        const bool one = tc::elect();
+        if (one) mbar_arrive_expect_tx(bar, C::kSlot);
+#pragma unroll
+        for (int w = 0; w < CT / 32; ++w) {
+#pragma unroll 1
+          for (int jj = 0; jj < 32 && 32 * w + jj < nbox; ++jj) {
+            const int j = 32 * w + jj, id = __shfl_sync(0xffffffffu, ids[w], jj);
+            const uint32_t to = dst + ((uint32_t)j << (box_log2 + 7));
+            if (j == part) {
+              for (int i = 0; i < box; ++i)
+                if (one)
+#pragma unroll
+                  for (int cb = 0; cb < CB; ++cb)
+                    tma_load_5d(to + cb * C::kBlock + i * 128, &p.tmv1, 0, (tb + (j << box_log2) + i) & slot_mask, cb,
+                                u.kvh, tb + (j << box_log2) + i < u.tok1 ? id : p.num_blocks, bar);
+            } else if (one) {
+#pragma unroll
+              for (int cb = 0; cb < CB; ++cb)
+                tma_load_5d(to + cb * C::kBlock, map, 0, (tb + (j << box_log2)) & slot_mask, cb, u.kvh, id, bar);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) filled[2 * slot + is_k] = item + 1;
+        if (c + 1 < u.chunks) fetch(c + 1);
+      }
+      base += 2 * u.chunks;
     }
-    if (lane == 0) {  // leave no copy in flight, whoever gives up
-      for (uint32_t i = item > NS ? item - NS : 0; i < item; ++i) wait(full + 8 * (i % NS), (i / NS) & 1, true);
+    if (is_k && lane == 0)  // leave no copy in flight, whoever gives up (K and V: below)
       for (int h = 0; h < 2; ++h)
         if (qn[h] > 0) wait(q_full + 8 * h, (qn[h] - 1) & 1, true);
-    }
   } else if (warp == C::kMmaWarp) {
     constexpr uint32_t IQK = tc::idesc(CT, false, false), IPV = tc::idesc(D, true, false);
     uint32_t item = 0, step = 0, qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0};
     int half = 0;
     bool ok = true;
+    auto all = [&](bool v) { return __all_sync(0xffffffffu, v) != 0; };
     SharedUnit u;
     for (int k = 0; ok && (ok = next_unit(k, u)) && u.chunks > 0; ++k) {
       const bool two = NACC == 2 && u.rows > kTileRows;
@@ -280,59 +301,61 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
       const int h = both || NACC == 1 ? 0 : half;
       if (!both && NACC == 2) half ^= 1;
       const int steps = two ? 2 * u.chunks : u.chunks;
-      if (lane == 0) {
-        auto k_item = [&](int c) { return item + (c == 0 ? 0 : 2 * c - 1); };
-        auto v_item = [&](int c) { return item + (c == u.chunks - 1 ? 2 * c + 1 : 2 * c + 2); };
-        auto qk = [&](int j) -> bool {
-          const int c = two ? j >> 1 : j, tile = two ? j & 1 : 0, buf = (step + j) & 1;
-          const uint32_t it = k_item(c), slot = it % NS;
-          if (!wait(full + 8 * slot, (it / NS) & 1)) return false;
-          tc::fence_after();
-          const uint32_t qb = sq + (h + tile) * (kTileRows * 128), kb = sring + slot * C::kSlot;
+      auto qk = [&](int j) -> bool {
+        const int c = two ? j >> 1 : j, tile = two ? j & 1 : 0, buf = (step + j) & 1;
+        const uint32_t it = item + (c == 0 ? 0 : 2 * c - 1), slot = it % NS;
+        if (!all(wait(full + 8 * slot, (it / NS) & 1))) return false;
+        tc::fence_after();
+        const uint64_t qd = tc::smem_desc(sq + (h + tile) * (kTileRows * 128), 16, 1024);
+        const uint64_t kd = tc::smem_desc(sring + slot * C::kSlot, 16, 1024);
+        if (tc::elect()) {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma_ss(tmem + buf * C::kSCol, tc::smem_desc(qb + (kk >> 2) * C::kQBlock + (kk & 3) * 32, 16, 1024),
-                       tc::smem_desc(kb + (kk >> 2) * C::kBlock + (kk & 3) * 32, 16, 1024), IQK, kk > 0);
+            tc::mma_ss(tmem + buf * C::kSCol, qd + (((kk >> 2) * C::kQBlock + (kk & 3) * 32) >> 4),
+                       kd + (((kk >> 2) * C::kBlock + (kk & 3) * 32) >> 4), IQK, kk > 0);
           tc::commit(s_full + 8 * buf);
           if (!two || tile == 1) tc::commit(empty + 8 * slot);
           if (j == steps - 1) {
             tc::commit(q_empty + 8 * h);
             if (both) tc::commit(q_empty + 8);
           }
-          return true;
-        };
-        auto pv = [&](int j) -> bool {
-          const int c = two ? j >> 1 : j, buf = (step + j) & 1, acc = NACC == 2 ? buf : 0;
-          const bool first = j < NACC;
-          const uint32_t it = v_item(c), slot = it % NS;
-          if (!wait(p_full + 8 * buf, pn[buf] & 1)) return false;
-          ++pn[buf];
-          if (!wait(full + 8 * slot, (it / NS) & 1)) return false;
-          if (first) {  // the last unit's sums have been read
-            if (on[acc] > 0 && !wait(o_free + 8 * acc, (on[acc] - 1) & 1)) return false;
-            ++on[acc];
-          }
-          tc::fence_after();
-          const uint32_t vb = sring + slot * C::kSlot;
+        }
+        __syncwarp();
+        return true;
+      };
+      auto pv = [&](int j) -> bool {
+        const int c = two ? j >> 1 : j, buf = (step + j) & 1, acc = NACC == 2 ? buf : 0;
+        const bool first = j < NACC;
+        const uint32_t it = item + (c == u.chunks - 1 ? 2 * c + 1 : 2 * c + 2), slot = it % NS;
+        if (first) {  // the last unit's sums have been read
+          if (on[acc] > 0 && !all(wait(o_free + 8 * acc, (on[acc] - 1) & 1))) return false;
+          ++on[acc];
+        }
+        if (!all(wait(full + 8 * slot, (it / NS) & 1))) return false;
+        if (!all(wait(p_full + 8 * buf, pn[buf] & 1))) return false;
+        ++pn[buf];
+        tc::fence_after();
+        const uint64_t vd = tc::smem_desc(sring + slot * C::kSlot, C::kBlock, 1024);
+        if (tc::elect()) {
 #pragma unroll
           for (int kk = 0; kk < CT / 16; ++kk)
-            tc::mma_ts(tmem + C::kOCol + acc * D, tmem + buf * C::kSCol + kk * 8,
-                       tc::smem_desc(vb + kk * 2048, C::kBlock, 1024), IPV, !first || kk > 0);
+            tc::mma_ts(tmem + C::kOCol + acc * D, tmem + buf * C::kSCol + kk * 8, vd + (kk * 2048 >> 4), IPV,
+                       !first || kk > 0);
           tc::commit(pv_done + 8 * acc);
           if (!two || (j & 1)) tc::commit(empty + 8 * slot);
-          return true;
-        };
-        ok = wait(q_full + 8 * h, qn[h] & 1) && (!both || wait(q_full + 8, qn[1] & 1));
-        ok = ok && qk(0) && (steps < 2 || qk(1));
-        for (int j = 0; ok && j < steps; ++j) ok = pv(j) && (j + 2 >= steps || qk(j + 2));
-      }
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+        }
+        __syncwarp();
+        return true;
+      };
+      ok = all(wait(q_full + 8 * h, qn[h] & 1)) && (!both || all(wait(q_full + 8, qn[1] & 1)));
+      ok = ok && qk(0) && (steps < 2 || qk(1));
+      for (int j = 0; ok && j < steps; ++j) ok = pv(j) && (j + 2 >= steps || qk(j + 2));
       ++qn[h];
       if (both) ++qn[1];
       item += 2 * u.chunks;
       step += steps;
     }
-    if (lane == 0) tc::commit(idle);  // every product issued above has completed when this arrives
+    if (tc::elect()) tc::commit(idle);  // every product issued above has completed when this arrives
   } else {
     // ---- softmax: thread = row of the group's tile
     const int w = warp >> 2, wq = warp & 3, row_in_tile = wq * 32 + lane;
@@ -360,28 +383,37 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
         if (live) {
           tc::fence_after();
           const uint32_t scol = lanes + buf * C::kSCol;
-          float s[CT];
+          const int nv = u.tok1 - (u.tok0 + (two ? j >> 1 : j) * CT);  // tokens of the chunk in range
+          // Scores are read twice, 32 columns at a time (a read is 32 cycles a warp),
+          // rather than kept: 128 of them and what the rest of the loop needs did
+          // not fit a thread's registers without spills.
+          const float none = sl2 >= 0.f ? -INFINITY : INFINITY;  // below every score
+          auto mask = [&](float *s, int at) {
+            if (at + 32 > nv) {
 #pragma unroll
-          for (int i = 0; i < CT; i += 32) tc::ld32(scol + i, s + i);
-          tc::wait_ld();
-          const int nv = u.tok1 - (u.tok0 + (two ? j >> 1 : j) * CT);
-          if (nv < CT) {  // the last chunk's tokens behind the range
+              for (int x = 0; x < 32; ++x)
+                if (at + x >= nv) s[x] = none;
+            }
+          };
+          float mx[4] = {none, none, none, none};
 #pragma unroll
-            for (int i = 0; i < CT; ++i)
-              if (i >= nv) s[i] = sl2 >= 0.f ? -INFINITY : INFINITY;
+          for (int i = 0; i < CT; i += 64) {
+            float s[64];
+            tc::ld32(scol + i, s);
+            tc::ld32(scol + i + 32, s + 32);
+            tc::wait_ld();
+            mask(s, i);
+            mask(s + 32, i + 32);
+            if (sl2 >= 0.f) {
+#pragma unroll
+              for (int x = 0; x < 64; x += 2) mx[x >> 1 & 3] = fmaxf(mx[x >> 1 & 3], fmaxf(s[x], s[x + 1]));
+            } else {
+#pragma unroll
+              for (int x = 0; x < 64; x += 2) mx[x >> 1 & 3] = fminf(mx[x >> 1 & 3], fminf(s[x], s[x + 1]));
+            }
           }
-          float mx[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) mx[i] = sl2 >= 0.f ? -INFINITY : INFINITY;
-          if (sl2 >= 0.f) {
-#pragma unroll
-            for (int i = 0; i < CT; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[i]);
-            mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          } else {
-#pragma unroll
-            for (int i = 0; i < CT; ++i) mx[i & 3] = fminf(mx[i & 3], s[i]);
-            mx[0] = fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3]));
-          }
+          mx[0] = sl2 >= 0.f ? fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]))
+                             : fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3]));
           const float top = mx[0] * sl2;
           // The reference moves only when a score passes it by 2^8: any
           // reference gives the same result as long as l and O share it, and the
@@ -395,30 +427,40 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
               ok = __all_sync(0xffffffffu, wait(pv_done + 8 * (NACC == 2 ? w : 0), (vn - 1) & 1));
               if (!ok) break;
               tc::fence_after();
-#pragma unroll
-              for (int i = 0; i < D; i += 32) {
-                float o[32];
-                tc::ld32(ocol + i, o);
+#pragma unroll 1
+              for (int i = 0; i < D; i += 16) {
+                float o[16];
+                tc::ld16(ocol + i, o);
                 tc::wait_ld();
 #pragma unroll
-                for (int x = 0; x < 32; ++x) o[x] *= a;
-                tc::st32(ocol + i, reinterpret_cast<const uint32_t *>(o));
+                for (int x = 0; x < 16; ++x) o[x] *= a;
+                tc::st16(ocol + i, reinterpret_cast<const uint32_t *>(o));
               }
             }
           }
           const float ref = m == -INFINITY ? 0.f : m;
-          uint32_t pk[CT / 2];
           float ls[4] = {0.f, 0.f, 0.f, 0.f};
+          float s[2][32];
+          tc::ld32(scol, s[0]);
+          tc::wait_ld();
+          // block i's 16 columns of P lie over columns that have been read
 #pragma unroll
-          for (int i = 0; i < CT; i += 2) {
-            const float e0 = fast_exp2(s[i] * sl2 - ref), e1 = fast_exp2(s[i + 1] * sl2 - ref);
-            ls[i & 2] += e0;
-            ls[(i & 2) + 1] += e1;
-            pk[i / 2] = pack_bf16x2(e0, e1);
+          for (int i = 0; i < CT; i += 32) {
+            float *cur = s[i / 32 & 1];
+            if (i + 32 < CT) tc::ld32(scol + i + 32, s[i / 32 + 1 & 1]);
+            mask(cur, i);
+            uint32_t pk[16];
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+              const float e0 = fast_exp2(cur[x] * sl2 - ref), e1 = fast_exp2(cur[x + 1] * sl2 - ref);
+              ls[x & 2] += e0;
+              ls[(x & 2) + 1] += e1;
+              pk[x / 2] = pack_bf16x2(e0, e1);
+            }
+            if (i + 32 < CT) tc::wait_ld();
+            tc::st16(scol + i / 2, pk);
           }
           l += (ls[0] + ls[1]) + (ls[2] + ls[3]);  // fp32 weights: rounded ones would move lse by up to 2^-9
-#pragma unroll
-          for (int i = 0; i < CT / 2; i += 32) tc::st32(scol + i, pk + i);
           tc::wait_st();
           tc::fence_before();
         }
@@ -457,7 +499,15 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
   tc::fence_before();
   __syncthreads();
   if (warp == 0) {
-    wait(idle, 0, true);  // no product may write tensor memory that is given back
+    // No copy is in flight when the CTA ends (an item is issued once its slot's
+    // earlier one has been read, so a slot's last item is the only one that can
+    // be), and no product writes tensor memory that is given back.
+    if (lane < NS) {
+      const uint32_t n = max(filled[2 * lane], filled[2 * lane + 1]);
+      if (n > 0) wait(full + 8 * lane, ((n - 1) / NS) & 1, true);
+    }
+    __syncwarp();
+    wait(idle, 0, true);
     tc::fence_after();
     tc::dealloc(tmem, 512);
   }
@@ -477,39 +527,99 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const __grid_constant
   const SharedPrefix pre = shared_prefix<D>(p);
   bool bad;
   const int L = shared_len(p, b, &bad), Lp = p.n_shared << p.bs_log2;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the partials and the cumulative costs are written
   const int64_t q = p.cum[p.B];
 
-  float m = -INFINITY, l = 0.f, acc[VEC];
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
-  auto add = [&](int64_t r) {
-    const float s = p.lse_part[r];
-    if (s == -INFINITY) return;
-    const float mn = fmaxf(m, s), a = exp2f(m - mn), w = exp2f(s - mn);
-    m = mn;
-    l = l * a + w;
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) acc[i] = acc[i] * a + w * p.o_part[r * D + lane * VEC + i];
+  // An item's candidate parts: (CTA, accumulator) pairs over the CTAs that its
+  // cost range touches; one that took no chunk is none.
+  struct Item {
+    int64_t start, cta0, part;  // cost, first CTA, part row of CTA 0 and row
+    int w, chunks, accs, stride, rows, n;
   };
-  auto item = [&](int64_t start, int64_t cost, int w, int chunks, int64_t part0, int stride, int rows, int r) {
-    const int accs = shared_part_rows(rows, D) / rows;
-    for (int64_t c = start / q; c <= (start + cost - 1) / q; ++c) {
-      const int n = shared_cut(p, (c + 1) * q - start, w, chunks) - shared_cut(p, c * q - start, w, chunks);
-      for (int a = 0; a < accs && a < n; ++a) add(part0 + c * stride + a * rows + r);
-    }
+  auto make = [&](int64_t start, int64_t cost, int w, int chunks, int64_t part0, int stride, int rows, int r) {
+    Item it;
+    it.start = start;
+    it.cta0 = start / q;
+    it.part = part0 + r;
+    it.w = w;
+    it.chunks = chunks;
+    it.accs = shared_part_rows(rows, D) / rows;
+    it.stride = stride;
+    it.rows = rows;
+    it.n = (int)((start + cost - 1) / q - it.cta0 + 1) * it.accs;
+    return it;
   };
+  Item pi{}, ri{};
   if (L > 0 && pre.chunks > 0) {
     const int grp = kvh * p.HT + ht, rb = b / p.nseq;
     const bool lastrb = rb == p.nrb - 1;
     const int rows = (lastrb ? pre.last_nb : p.nseq) * p.gt;
-    item(grp * pre.group + rb * pre.full, lastrb ? pre.last : pre.full, rows > kTileRows ? p.w_pre2 : p.w_pre1,
-         pre.chunks, ((int64_t)grp * p.nrb + rb) * p.pre_rows, p.pre_rows, rows, (b - rb * p.nseq) * p.gt + j);
+    pi = make(grp * pre.group + rb * pre.full, lastrb ? pre.last : pre.full, rows > kTileRows ? p.w_pre2 : p.w_pre1,
+              pre.chunks, ((int64_t)grp * p.nrb + rb) * p.pre_rows, p.pre_rows, rows, (b - rb * p.nseq) * p.gt + j);
   }
   if (L > Lp) {
     const int64_t cost = shared_rest_cost<D>(p, L);
     const int k = kvh * p.HT + ht;
-    item(p.cum[b] + k * cost, cost, p.w_rest, (L - Lp + shared_chunk(D) - 1) / shared_chunk(D),
-         p.rest_row0 + ((int64_t)b * p.Hkv * p.HT + k) * p.rest_rows, p.rest_rows, p.gt, j);
+    ri = make(p.cum[b] + k * cost, cost, p.w_rest, (L - Lp + shared_chunk(D) - 1) / shared_chunk(D),
+              p.rest_row0 + ((int64_t)b * p.Hkv * p.HT + k) * p.rest_rows, p.rest_rows, p.gt, j);
+  }
+  float m = -INFINITY, l = 0.f, acc[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
+  for (int i0 = 0; i0 < pi.n + ri.n; i0 += 32) {  // lane: one candidate
+    const int i = i0 + lane;
+    float s = -INFINITY;
+    int64_t r = 0;
+    if (i < pi.n + ri.n) {
+      const Item &it = i < pi.n ? pi : ri;
+      const int x = i < pi.n ? i : i - pi.n;
+      const int64_t c = it.cta0 + x / it.accs;
+      const int a = x % it.accs;
+      const int n = shared_cut(p, (c + 1) * q - it.start, it.w, it.chunks) - shared_cut(p, c * q - it.start, it.w, it.chunks);
+      if (a < n) {
+        r = it.part + c * it.stride + a * it.rows;
+        s = p.lse_part[r];
+      }
+    }
+    float top = s;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    const float mn = fmaxf(m, top), ref = mn == -INFINITY ? 0.f : mn;
+    const float a = exp2f(m - ref), w = exp2f(s - ref);
+    float sum = w;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    l = l * a + sum;
+    m = mn;
+#pragma unroll
+    for (int x = 0; x < VEC; ++x) acc[x] *= a;
+    uint32_t todo = __ballot_sync(0xffffffffu, s != -INFINITY);
+    while (todo != 0) {  // four partials in flight
+      float o[4][VEC], wj[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int jl = todo != 0 ? __ffs(todo) - 1 : 0;
+        const int64_t rj = __shfl_sync(0xffffffffu, r, jl);
+        wj[y] = todo != 0 ? __shfl_sync(0xffffffffu, w, jl) : 0.f;
+        if (todo != 0) {
+          const float *src = p.o_part + rj * D + lane * VEC;
+#pragma unroll
+          for (int x = 0; x < VEC; x += 2) {
+            const float2 f = *reinterpret_cast<const float2 *>(src + x);
+            o[y][x] = f.x;
+            o[y][x + 1] = f.y;
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < VEC; ++x) o[y][x] = 0.f;
+        }
+        todo &= todo - 1;
+      }
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+#pragma unroll
+        for (int x = 0; x < VEC; ++x) acc[x] += wj[y] * o[y][x];
+    }
   }
   float lse2 = m + log2f(l);  // no token: m = -inf
   if (p.sinks != nullptr) {
@@ -547,8 +657,17 @@ cudaError_t launch_t(const SharedParams &p, cudaStream_t s) {
   }
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int64_t rows = (int64_t)p.B * p.Hq;
-  shared_merge_kernel<D><<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(p);
-  return cudaGetLastError();
+  // comes up while the partial kernel's last CTAs run; waits for them before its first read
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, shared_merge_kernel<D>, p);
 }
 
 }  // namespace
