@@ -74,13 +74,13 @@ __global__ void __launch_bounds__(256) shared_kernel(const __grid_constant__ Sha
 // units in order, each as far ahead as its buffers let it:
 //
 //   schedule warp   walks the work line and puts units into a queue of kQueue
-//   copy warps      TMA of the unit's q rows and K chunks, and of its V chunks, into
-//                   one ring (items K0 K1 V0 K2 V1 ...), boxes of one 128-byte column
-//                   block x one page (or a chunk's worth of a larger page)
+//   copy warps      TMA of the unit's q rows and K chunks into one ring, and of its V
+//                   chunks into another, boxes of one 128-byte column block x one page
+//                   (or a chunk's worth of a larger page)
 //   MMA warp        S = Q . K^T  (128 rows x chunk) into one of two S buffers, then
 //                   O += P . V  with P read from tensor memory
-//   softmax warps   thread = row: scores out of tensor memory, running maximum and
-//                   sum, P back over the scores it was made from
+//   softmax warps   two threads per row, half a chunk's columns each: scores out of
+//                   tensor memory, running maximum and sum, P back over the scores
 //
 // A step is (query tile, chunk): S buffer of a step = its parity, so one step's
 // softmax runs under the other's products.  A two-tile unit takes both tiles
@@ -99,9 +99,12 @@ struct SharedCfg {
   static constexpr uint32_t kBlock = CT * 128;          // one column block of it
   static constexpr uint32_t kQBlock = QR * 128;         // one column block of q
   static constexpr uint32_t kQ = CB * kQBlock;
-  static constexpr int NS = D == 64 ? 8 : 5;            // ring slots
+  // Ring slots: what is left beside q.  V's slots are held longer, from the copy
+  // to the value product two steps behind the score product.
+  static constexpr int NK = D == 64 ? 4 : 2, NV = D == 64 ? 4 : 3, NS = NK + NV;
   static constexpr int kQueue = 4;
-  static constexpr int kSoftmaxWarps = 4 * NACC;
+  static constexpr int kGroupWarps = 8;                 // a softmax group: 4 x 32 rows, two halves of the columns
+  static constexpr int kSoftmaxWarps = kGroupWarps * NACC;
   static constexpr int kCopyKWarp = kSoftmaxWarps, kCopyVWarp = kSoftmaxWarps + 1, kMmaWarp = kSoftmaxWarps + 2,
                        kScheduleWarp = kSoftmaxWarps + 3;
   static constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
@@ -127,25 +130,23 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
                  s_full = q_empty + 16, p_full = s_full + 16, pv_done = p_full + 16, o_free = pv_done + 16,
                  u_full = o_free + 16, u_empty = u_full + 8 * C::kQueue, idle = u_empty + 8 * C::kQueue;
   constexpr int kBars = 2 * NS + 12 + 2 * C::kQueue + 1;
-  static_assert(kBars * 8 + 8 + 8 * NS <= 512, "barrier area");
+  static_assert(kBars * 8 + 8 <= 512, "barrier area");
   uint32_t *words = reinterpret_cast<uint32_t *>(bars + kBars);  // [0] tmem, [1] abort
   volatile int *abort_flag = reinterpret_cast<volatile int *>(words + 1);
-  uint32_t *filled = words + 2;  // [NS][2] 1 + the last item that each copy warp put into a slot
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 1);
-      filled[2 * i] = filled[2 * i + 1] = 0;
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + 8 * i, 1);
       mbar_init(q_empty + 8 * i, 1);
       mbar_init(s_full + 8 * i, 1);
-      mbar_init(p_full + 8 * i, 4);   // a softmax group's warps
+      mbar_init(p_full + 8 * i, C::kGroupWarps);
       mbar_init(pv_done + 8 * i, 1);
-      mbar_init(o_free + 8 * i, 4);
+      mbar_init(o_free + 8 * i, C::kGroupWarps);
     }
     for (int i = 0; i < C::kQueue; ++i) {
       mbar_init(u_full + 8 * i, 1);
@@ -201,7 +202,8 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
     const CUtensorMap *map = is_k ? &p.tmk : &p.tmv;
     const int box_log2 = min(p.bs_log2, CT == 128 ? 7 : 6), box = 1 << box_log2, nbox = CT >> box_log2;
     const int slot_mask = (1 << p.bs_log2) - 1;
-    uint32_t base = 0;               // ring items of the units before this one
+    const int first_slot = is_k ? 0 : C::NK, slots = is_k ? C::NK : C::NV;
+    uint32_t item = 0;               // chunks copied
     uint32_t qn[2] = {0, 0};         // uses of each half of q
     int half = 0;
     bool ok = true;
@@ -246,9 +248,8 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
       }
       // ---- this warp's chunks
       for (int c = 0; ok && c < u.chunks; ++c) {
-        const uint32_t item = base + (is_k ? (c == 0 ? 0 : 2 * c - 1) : c == u.chunks - 1 ? 2 * c + 1 : 2 * c + 2);
-        const int slot = item % NS;
-        if (item >= NS && !__all_sync(0xffffffffu, wait(empty + 8 * slot, (item / NS - 1) & 1))) {
+        const int slot = first_slot + item % slots;
+        if (item >= slots && !__all_sync(0xffffffffu, wait(empty + 8 * slot, (item / slots - 1) & 1))) {
           ok = false;
           break;
         }
@@ -280,87 +281,149 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
           }
         }
         __syncwarp();
-        if (lane == 0) filled[2 * slot + is_k] = item + 1;
+        ++item;
         if (c + 1 < u.chunks) fetch(c + 1);
       }
-      base += 2 * u.chunks;
     }
-    if (is_k && lane == 0)  // leave no copy in flight, whoever gives up (K and V: below)
+    // Leave no copy in flight, whoever gives up: a chunk is copied once its slot's
+    // earlier one has been read, so only the last `slots` can be open.
+    if (lane == 0) {
+      for (uint32_t i = item > (uint32_t)slots ? item - slots : 0; i < item; ++i)
+        wait(full + 8 * (first_slot + i % slots), (i / slots) & 1, true);
       for (int h = 0; h < 2; ++h)
         if (qn[h] > 0) wait(q_full + 8 * h, (qn[h] - 1) & 1, true);
+    }
   } else if (warp == C::kMmaWarp) {
     constexpr uint32_t IQK = tc::idesc(CT, false, false), IPV = tc::idesc(D, true, false);
-    uint32_t item = 0, step = 0, qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0};
+    // Two cursors over the CTA's steps, the score product's up to two steps ahead
+    // of the value product's (there are two S buffers), across units.
+    struct Cursor {
+      int k, j, steps, chunks, h;   // next unit of the queue; step of the unit; its q half
+      uint32_t item, step;          // chunks and steps of the units before it
+      bool two, both;
+    };
+    Cursor cq{-1, 0, 0, 0, 0, 0, 0, false, false}, cp = cq;
+    uint32_t qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0};
     int half = 0;
-    bool ok = true;
+    bool ok = true, more = true;
     auto all = [&](bool v) { return __all_sync(0xffffffffu, v) != 0; };
     SharedUnit u;
-    for (int k = 0; ok && (ok = next_unit(k, u)) && u.chunks > 0; ++k) {
-      const bool two = NACC == 2 && u.rows > kTileRows;
-      const bool both = NACC == 2 && q_box_rows(u) > kTileRows;
-      const int h = both || NACC == 1 ? 0 : half;
-      if (!both && NACC == 2) half ^= 1;
-      const int steps = two ? 2 * u.chunks : u.chunks;
-      auto qk = [&](int j) -> bool {
-        const int c = two ? j >> 1 : j, tile = two ? j & 1 : 0, buf = (step + j) & 1;
-        const uint32_t it = item + (c == 0 ? 0 : 2 * c - 1), slot = it % NS;
-        if (!all(wait(full + 8 * slot, (it / NS) & 1))) return false;
-        tc::fence_after();
-        const uint64_t qd = tc::smem_desc(sq + (h + tile) * (kTileRows * 128), 16, 1024);
-        const uint64_t kd = tc::smem_desc(sring + slot * C::kSlot, 16, 1024);
-        if (tc::elect()) {
+    int queued_steps[2], queued_chunks[2];  // the units between the cursors: at most two, by parity
+    bool queued_two[2];
+    // The score product's cursor on its next step; false: no unit left (or gave up).
+    auto next_qk = [&]() -> bool {
+      if (cq.j < cq.steps) return true;
+      if (!more) return false;
+      cq.item += cq.chunks;
+      cq.step += cq.steps;
+      ++cq.k;
+      ok = next_unit(cq.k, u);
+      if (!ok || u.chunks == 0) {
+        more = false;
+        cq.steps = cq.chunks = cq.j = 0;
+        return false;
+      }
+      cq.two = NACC == 2 && u.rows > kTileRows;
+      cq.both = NACC == 2 && q_box_rows(u) > kTileRows;
+      cq.h = cq.both || NACC == 1 ? 0 : half;
+      if (!cq.both && NACC == 2) half ^= 1;
+      cq.chunks = u.chunks;
+      cq.steps = cq.two ? 2 * u.chunks : u.chunks;
+      cq.j = 0;
+      queued_steps[cq.k & 1] = cq.steps;
+      queued_chunks[cq.k & 1] = cq.chunks;
+      queued_two[cq.k & 1] = cq.two;
+      ok = all(wait(q_full + 8 * cq.h, qn[cq.h] & 1)) && (!cq.both || all(wait(q_full + 8, qn[1] & 1)));
+      ++qn[cq.h];
+      if (cq.both) ++qn[1];
+      return ok;
+    };
+    auto qk = [&]() -> bool {
+      const int c = cq.two ? cq.j >> 1 : cq.j, tile = cq.two ? cq.j & 1 : 0, buf = (cq.step + cq.j) & 1;
+      const uint32_t it = cq.item + c, slot = it % C::NK;
+      if (!all(wait(full + 8 * slot, (it / C::NK) & 1))) return false;
+      tc::fence_after();
+      const uint64_t qd = tc::smem_desc(sq + (cq.h + tile) * (kTileRows * 128), 16, 1024);
+      const uint64_t kd = tc::smem_desc(sring + slot * C::kSlot, 16, 1024);
+      if (tc::elect()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma_ss(tmem + buf * C::kSCol, qd + (((kk >> 2) * C::kQBlock + (kk & 3) * 32) >> 4),
-                       kd + (((kk >> 2) * C::kBlock + (kk & 3) * 32) >> 4), IQK, kk > 0);
-          tc::commit(s_full + 8 * buf);
-          if (!two || tile == 1) tc::commit(empty + 8 * slot);
-          if (j == steps - 1) {
-            tc::commit(q_empty + 8 * h);
-            if (both) tc::commit(q_empty + 8);
-          }
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc::mma_ss(tmem + buf * C::kSCol, qd + (((kk >> 2) * C::kQBlock + (kk & 3) * 32) >> 4),
+                     kd + (((kk >> 2) * C::kBlock + (kk & 3) * 32) >> 4), IQK, kk > 0);
+        tc::commit(s_full + 8 * buf);
+        if (!cq.two || tile == 1) tc::commit(empty + 8 * slot);
+        if (cq.j == cq.steps - 1) {
+          tc::commit(q_empty + 8 * cq.h);
+          if (cq.both) tc::commit(q_empty + 8);
         }
-        __syncwarp();
-        return true;
-      };
-      auto pv = [&](int j) -> bool {
-        const int c = two ? j >> 1 : j, buf = (step + j) & 1, acc = NACC == 2 ? buf : 0;
-        const bool first = j < NACC;
-        const uint32_t it = item + (c == u.chunks - 1 ? 2 * c + 1 : 2 * c + 2), slot = it % NS;
-        if (first) {  // the last unit's sums have been read
-          if (on[acc] > 0 && !all(wait(o_free + 8 * acc, (on[acc] - 1) & 1))) return false;
-          ++on[acc];
-        }
-        if (!all(wait(full + 8 * slot, (it / NS) & 1))) return false;
-        if (!all(wait(p_full + 8 * buf, pn[buf] & 1))) return false;
-        ++pn[buf];
-        tc::fence_after();
-        const uint64_t vd = tc::smem_desc(sring + slot * C::kSlot, C::kBlock, 1024);
-        if (tc::elect()) {
+      }
+      __syncwarp();
+      ++cq.j;
+      return true;
+    };
+    auto pv = [&]() -> bool {
+      if (cp.j == cp.steps) {  // on to the next unit, which the other cursor has been given
+        cp.item += cp.chunks;
+        cp.step += cp.steps;
+        ++cp.k;
+        cp.steps = queued_steps[cp.k & 1];
+        cp.chunks = queued_chunks[cp.k & 1];
+        cp.two = queued_two[cp.k & 1];
+        cp.j = 0;
+      }
+      const int c = cp.two ? cp.j >> 1 : cp.j, buf = (cp.step + cp.j) & 1, acc = NACC == 2 ? buf : 0;
+      const bool first = cp.j < NACC;
+      const uint32_t it = cp.item + c, slot = C::NK + it % C::NV;
+      if (first) {  // the last unit's sums have been read
+        if (on[acc] > 0 && !all(wait(o_free + 8 * acc, (on[acc] - 1) & 1))) return false;
+        ++on[acc];
+      }
+      if (!all(wait(full + 8 * slot, (it / C::NV) & 1))) return false;
+      if (!all(wait(p_full + 8 * buf, pn[buf] & 1))) return false;
+      ++pn[buf];
+      tc::fence_after();
+      const uint64_t vd = tc::smem_desc(sring + slot * C::kSlot, C::kBlock, 1024);
+      if (tc::elect()) {
 #pragma unroll
-          for (int kk = 0; kk < CT / 16; ++kk)
-            tc::mma_ts(tmem + C::kOCol + acc * D, tmem + buf * C::kSCol + kk * 8, vd + (kk * 2048 >> 4), IPV,
-                       !first || kk > 0);
-          tc::commit(pv_done + 8 * acc);
-          if (!two || (j & 1)) tc::commit(empty + 8 * slot);
-        }
-        __syncwarp();
-        return true;
-      };
-      ok = all(wait(q_full + 8 * h, qn[h] & 1)) && (!both || all(wait(q_full + 8, qn[1] & 1)));
-      ok = ok && qk(0) && (steps < 2 || qk(1));
-      for (int j = 0; ok && j < steps; ++j) ok = pv(j) && (j + 2 >= steps || qk(j + 2));
-      ++qn[h];
-      if (both) ++qn[1];
-      item += 2 * u.chunks;
-      step += steps;
+        for (int kk = 0; kk < CT / 16; ++kk)
+          tc::mma_ts(tmem + C::kOCol + acc * D, tmem + buf * C::kSCol + kk * 8, vd + (kk * 2048 >> 4), IPV,
+                     !first || kk > 0);
+        tc::commit(pv_done + 8 * acc);
+        if (!cp.two || (cp.j & 1)) tc::commit(empty + 8 * slot);
+      }
+      __syncwarp();
+      ++cp.j;
+      return true;
+    };
+    int ahead = 0;
+    while (ok) {
+      while (ok && ahead < 2 && next_qk()) {
+        ok = qk();
+        ++ahead;
+      }
+      if (!ok || ahead == 0) break;
+      ok = pv();
+      --ahead;
     }
     if (tc::elect()) tc::commit(idle);  // every product issued above has completed when this arrives
   } else {
-    // ---- softmax: thread = row of the group's tile
-    const int w = warp >> 2, wq = warp & 3, row_in_tile = wq * 32 + lane;
+    // ---- softmax: a row's columns in two halves, one thread each
+    constexpr int HC = CT / 2;
+    const int w = warp / C::kGroupWarps, half = warp >> 2 & 1, wq = warp & 3, row_in_tile = wq * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
+    const uint32_t ocol = lanes + C::kOCol + w * D + half * (D / 2);
+    // The two warps of the same rows exchange a value per row through a column of
+    // tensor memory each (shared memory is full): own, then a barrier, then other.
+    auto exchange = [&](uint32_t own, uint32_t other, float v) -> float {
+      tc::st1(own, v);
+      tc::wait_st();
+      tc::fence_before();
+      asm volatile("bar.sync %0, 64;\n" ::"r"(1 + w * 4 + wq) : "memory");
+      tc::fence_after();
+      return tc::ld1(other);
+    };
     const float sl2 = p.scale_log2;
+    const float none = sl2 >= 0.f ? -INFINITY : INFINITY;  // below every score
     uint32_t step = 0;               // steps of all units so far
     uint32_t sn[2] = {0, 0};         // S buffer uses
     uint32_t vn = 0;                 // products into this group's accumulator
@@ -373,7 +436,6 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
       const int tile = two ? j0 : 0;
       const int r = tile * kTileRows + row_in_tile;
       const bool live = tile * kTileRows + wq * 32 < u.rows;  // the warp has a row
-      const uint32_t ocol = lanes + C::kOCol + (NACC == 2 ? w : 0) * D;
       float m = -INFINITY, l = 0.f;
       for (int j = j0; ok && j < steps; j += NACC) {
         const int buf = (int)(step + j) & 1;
@@ -383,38 +445,31 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
         if (live) {
           tc::fence_after();
           const uint32_t scol = lanes + buf * C::kSCol;
-          const int nv = u.tok1 - (u.tok0 + (two ? j >> 1 : j) * CT);  // tokens of the chunk in range
-          // Scores are read twice, 32 columns at a time (a read is 32 cycles a warp),
-          // rather than kept: 128 of them and what the rest of the loop needs did
-          // not fit a thread's registers without spills.
-          const float none = sl2 >= 0.f ? -INFINITY : INFINITY;  // below every score
-          auto mask = [&](float *s, int at) {
-            if (at + 32 > nv) {
+          float s[HC];
 #pragma unroll
-              for (int x = 0; x < 32; ++x)
-                if (at + x >= nv) s[x] = none;
-            }
-          };
-          float mx[4] = {none, none, none, none};
+          for (int i = 0; i < HC; i += 32) tc::ld32(scol + half * HC + i, s + i);
+          tc::wait_ld();
+          const int nv = u.tok1 - (u.tok0 + (two ? j >> 1 : j) * CT) - half * HC;  // columns in range
+          if (nv < HC) {
 #pragma unroll
-          for (int i = 0; i < CT; i += 64) {
-            float s[64];
-            tc::ld32(scol + i, s);
-            tc::ld32(scol + i + 32, s + 32);
-            tc::wait_ld();
-            mask(s, i);
-            mask(s + 32, i + 32);
-            if (sl2 >= 0.f) {
-#pragma unroll
-              for (int x = 0; x < 64; x += 2) mx[x >> 1 & 3] = fmaxf(mx[x >> 1 & 3], fmaxf(s[x], s[x + 1]));
-            } else {
-#pragma unroll
-              for (int x = 0; x < 64; x += 2) mx[x >> 1 & 3] = fminf(mx[x >> 1 & 3], fminf(s[x], s[x + 1]));
-            }
+            for (int i = 0; i < HC; ++i)
+              if (i >= nv) s[i] = none;
           }
-          mx[0] = sl2 >= 0.f ? fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]))
-                             : fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3]));
-          const float top = mx[0] * sl2;
+          float mx[4] = {none, none, none, none};
+          if (sl2 >= 0.f) {
+#pragma unroll
+            for (int i = 0; i < HC; i += 2) mx[i >> 1 & 3] = fmaxf(mx[i >> 1 & 3], fmaxf(s[i], s[i + 1]));
+            mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < HC; i += 2) mx[i >> 1 & 3] = fminf(mx[i >> 1 & 3], fminf(s[i], s[i + 1]));
+            mx[0] = fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3]));
+          }
+          // Each half's maximum travels in its last column of S, which it has read.
+          // Behind the exchange all of S has been read: P, in its first half, may
+          // overwrite it.
+          float top = mx[0] * sl2;
+          top = fmaxf(top, exchange(scol + half * HC + HC - 1, scol + (half ^ 1) * HC + HC - 1, top));
           // The reference moves only when a score passes it by 2^8: any
           // reference gives the same result as long as l and O share it, and the
           // rescale of O is skipped on almost every chunk.
@@ -424,11 +479,11 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
             m = mn;
             l *= a;
             if (j != j0) {  // O holds the earlier chunks once their product is done
-              ok = __all_sync(0xffffffffu, wait(pv_done + 8 * (NACC == 2 ? w : 0), (vn - 1) & 1));
+              ok = __all_sync(0xffffffffu, wait(pv_done + 8 * w, (vn - 1) & 1));
               if (!ok) break;
               tc::fence_after();
 #pragma unroll 1
-              for (int i = 0; i < D; i += 16) {
+              for (int i = 0; i < D / 2; i += 16) {
                 float o[16];
                 tc::ld16(ocol + i, o);
                 tc::wait_ld();
@@ -440,27 +495,20 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
           }
           const float ref = m == -INFINITY ? 0.f : m;
           float ls[4] = {0.f, 0.f, 0.f, 0.f};
-          float s[2][32];
-          tc::ld32(scol, s[0]);
-          tc::wait_ld();
-          // block i's 16 columns of P lie over columns that have been read
 #pragma unroll
-          for (int i = 0; i < CT; i += 32) {
-            float *cur = s[i / 32 & 1];
-            if (i + 32 < CT) tc::ld32(scol + i + 32, s[i / 32 + 1 & 1]);
-            mask(cur, i);
+          for (int i = 0; i < HC; i += 32) {
             uint32_t pk[16];
 #pragma unroll
             for (int x = 0; x < 32; x += 2) {
-              const float e0 = fast_exp2(cur[x] * sl2 - ref), e1 = fast_exp2(cur[x + 1] * sl2 - ref);
+              const float e0 = fast_exp2(s[i + x] * sl2 - ref), e1 = fast_exp2(s[i + x + 1] * sl2 - ref);
               ls[x & 2] += e0;
               ls[(x & 2) + 1] += e1;
               pk[x / 2] = pack_bf16x2(e0, e1);
             }
-            if (i + 32 < CT) tc::wait_ld();
-            tc::st16(scol + i / 2, pk);
+            tc::st16(scol + (half * HC + i) / 2, pk);
           }
           l += (ls[0] + ls[1]) + (ls[2] + ls[3]);  // fp32 weights: rounded ones would move lse by up to 2^-9
+          if (j + NACC >= steps) l += exchange(scol + HC + half, scol + HC + (half ^ 1), l);  // the unit's sum
           tc::wait_st();
           tc::fence_before();
         }
@@ -469,14 +517,17 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
         if (lane == 0) tc::arrive(p_full + 8 * buf);
       }
       if (ok && steps > j0) {
-        ok = __all_sync(0xffffffffu, wait(pv_done + 8 * (NACC == 2 ? w : 0), (vn - 1) & 1));
+        // (a parity tells only neighbouring phases apart: with one accumulator the
+        // last two products may both be open)
+        if (NACC == 1 && steps > 1) ok = __all_sync(0xffffffffu, wait(pv_done + 8 * w, (vn - 2) & 1));
+        ok = ok && __all_sync(0xffffffffu, wait(pv_done + 8 * w, (vn - 1) & 1));
         if (ok && live) {
           tc::fence_after();
           const float inv = 1.f / l;
           const int64_t row = u.part + (two || NACC == 1 ? 0 : (int64_t)j0 * u.rows) + r;
-          float4 *dst = reinterpret_cast<float4 *>(p.o_part + row * D);
+          float4 *dst = reinterpret_cast<float4 *>(p.o_part + row * D + half * (D / 2));
 #pragma unroll
-          for (int i = 0; i < D; i += 32) {
+          for (int i = 0; i < D / 2; i += 32) {
             float o[32];
             tc::ld32(ocol + i, o);
             tc::wait_ld();
@@ -486,11 +537,11 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
                 dst[i / 4 + x] = make_float4(o[4 * x] * inv, o[4 * x + 1] * inv, o[4 * x + 2] * inv, o[4 * x + 3] * inv);
             }
           }
-          if (r < u.rows) p.lse_part[row] = m + log2f(l);
+          if (half == 0 && r < u.rows) p.lse_part[row] = m + log2f(l);
           tc::fence_before();
         }
         __syncwarp();
-        if (lane == 0) tc::arrive(o_free + 8 * (NACC == 2 ? w : 0));
+        if (lane == 0) tc::arrive(o_free + 8 * w);
       }
       step += steps;
     }
@@ -499,15 +550,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
   tc::fence_before();
   __syncthreads();
   if (warp == 0) {
-    // No copy is in flight when the CTA ends (an item is issued once its slot's
-    // earlier one has been read, so a slot's last item is the only one that can
-    // be), and no product writes tensor memory that is given back.
-    if (lane < NS) {
-      const uint32_t n = max(filled[2 * lane], filled[2 * lane + 1]);
-      if (n > 0) wait(full + 8 * lane, ((n - 1) / NS) & 1, true);
-    }
-    __syncwarp();
-    wait(idle, 0, true);
+    wait(idle, 0, true);  // no product may write tensor memory that is given back
     tc::fence_after();
     tc::dealloc(tmem, 512);
   }
@@ -539,14 +582,14 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const __grid_constant
   auto make = [&](int64_t start, int64_t cost, int w, int chunks, int64_t part0, int stride, int rows, int r) {
     Item it;
     it.start = start;
-    it.cta0 = start / q;
+    it.cta0 = shared_div(start, q);
     it.part = part0 + r;
     it.w = w;
     it.chunks = chunks;
     it.accs = shared_part_rows(rows, D) / rows;
     it.stride = stride;
     it.rows = rows;
-    it.n = (int)((start + cost - 1) / q - it.cta0 + 1) * it.accs;
+    it.n = (int)(shared_div(start + cost - 1, q) - it.cta0 + 1) * it.accs;
     return it;
   };
   Item pi{}, ri{};

@@ -17,6 +17,12 @@ struct SharedUnit {
   int64_t part;         // first part row
 };
 
+// Costs fit 32 bits but for the very largest problems, and a 64-bit division is
+// tens of instructions.
+__device__ __forceinline__ int64_t shared_div(int64_t a, int64_t b) {
+  return ((uint64_t)a | (uint64_t)b) >> 32 == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // A sequence's length as the kernels use it: outside [0, capacity], or shorter
 // than the prefix it claims, is an error; it counts as the nearest valid one (0
 // for a sequence shorter than the prefix).
@@ -58,7 +64,7 @@ __device__ __forceinline__ SharedPrefix shared_prefix(const SharedParams &p) {
 // First chunk of an item at or behind `at` (a cost counted from the item's start).
 __device__ __forceinline__ int shared_cut(const SharedParams &p, int64_t at, int w, int chunks) {
   if (at <= p.w_item) return 0;
-  const int64_t c = (at - p.w_item + w - 1) / w;
+  const int64_t c = shared_div(at - p.w_item + w - 1, w);
   return c > chunks ? chunks : (int)c;
 }
 
@@ -81,14 +87,14 @@ __device__ __forceinline__ void shared_walk(const SharedParams &p, int cta, int6
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
   const int64_t total = pre.total + sum;
-  const int64_t q = (total + p.ctas - 1) / p.ctas;
+  const int64_t q = shared_div(total + p.ctas - 1, p.ctas);
   int64_t pos = cta * q;
   const int64_t end = pos + q < total ? pos + q : total;
 
   while (pos < end && pos < pre.total) {
-    const int grp = (int)(pos / pre.group);
+    const int grp = (int)shared_div(pos, pre.group);
     const int64_t in = pos - grp * pre.group;
-    int rb = (int)(in / pre.full);
+    int rb = (int)shared_div(in, pre.full);
     if (rb > p.nrb - 1) rb = p.nrb - 1;
     const int64_t start = grp * pre.group + rb * pre.full;
     const int64_t cost = rb == p.nrb - 1 ? pre.last : pre.full;
@@ -136,7 +142,7 @@ __device__ __forceinline__ void shared_walk(const SharedParams &p, int cta, int6
       const int Lj = __shfl_sync(0xffffffffu, L, j);
       const int chunks = (Lj - Lp + CT - 1) / CT;
       while (pos < end && pos < f + it * hh) {
-        const int k = (int)((pos - f) / it);
+        const int k = (int)shared_div(pos - f, it);
         const int64_t start = f + k * it;
         SharedUnit u;
         u.rest = 1;

@@ -48,6 +48,9 @@ CASES = {
     "d256_pages_of_256": (2, 8, 2, 256, 256, 1, [70, 300], {}),
     "long_prefix": (4, 8, 2, 128, 16, 500, [20, 0, 1, 300], {}),
     "long_rest": (3, 8, 2, 128, 16, 2, [5000, 1, 0], {}),
+    "many_long": (40, 40, 8, 128, 16, 0, [13 * i + 1 for i in range(40)], {}),
+    "many_long_d64": (40, 16, 4, 64, 16, 5, [17 * i for i in range(40)], {}),
+    "many_long_d256": (40, 16, 4, 256, 16, 0, [13 * i + 1 for i in range(40)], {}),
     "wide_scores": (4, 8, 2, 128, 16, 30, [200, 90, 0, 5], {"k_amp": 12.0}),
 }
 
