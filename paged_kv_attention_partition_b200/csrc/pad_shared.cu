@@ -68,35 +68,90 @@ __global__ void __launch_bounds__(256) shared_kernel(const __grid_constant__ Sha
   });
 }
 
+// ---- arithmetic of the softmax, two values at a time ----------------------------
+
+__device__ __forceinline__ uint64_t duo(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 parts(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// 2^x of two values on the FMA pipe: x = n + f with n the nearest integer (the low
+// bits of x + 1.5 * 2^23), 2^f by the degree-5 polynomial that interpolates it at
+// the Chebyshev nodes of [-1/2, 1/2] (2.5e-7 off at most), 2^n by its exponent
+// field.  Below -126.5 it is 0; NaN stays NaN.
+__device__ __forceinline__ float2 exp2_fma(uint64_t x) {
+  const float2 xc = parts(x);
+  const uint64_t c = duo(max_nan(xc.x, -127.f), max_nan(xc.y, -127.f));
+  const uint64_t t = add2(c, duo(12582912.f, 12582912.f));
+  const uint64_t f = add2(c, mul2(add2(t, duo(-12582912.f, -12582912.f)), duo(-1.f, -1.f)));
+  uint64_t p = duo(0.0013390863f, 0.0013390863f);
+  p = fma2(p, f, duo(0.009676032f, 0.009676032f));
+  p = fma2(p, f, duo(0.05550357f, 0.05550357f));
+  p = fma2(p, f, duo(0.24022107f, 0.24022107f));
+  p = fma2(p, f, duo(0.6931472f, 0.6931472f));
+  p = fma2(p, f, duo(1.0000001f, 1.0000001f));
+  const float2 ti = parts(t);
+  return parts(mul2(p, duo(__uint_as_float((__float_as_uint(ti.x) << 23) + 0x3f800000u),
+                           __uint_as_float((__float_as_uint(ti.y) << 23) + 0x3f800000u))));
+}
+
 // ---- the partial kernel -------------------------------------------------------
 //
 // One persistent CTA per SM, warp-specialised; every role goes through the CTA's
 // units in order, each as far ahead as its buffers let it:
 //
-//   schedule warp   walks the work line and puts units into a queue of kQueue
-//   copy warps      TMA of the unit's q rows and K chunks into one ring, and of its V
-//                   chunks into another, boxes of one 128-byte column block x one page
-//                   (or a chunk's worth of a larger page)
-//   MMA warp        S = Q . K^T  (128 rows x chunk) into one of two S buffers, then
-//                   O += P . V  with P read from tensor memory
+//   K warp          walks the work line, puts units into a queue of kQueue, copies
+//                   (TMA) the unit's q rows, and its K chunks into a ring
+//   V warp          the V chunks into another ring
+//   QK warp         S = Q . K^T  (128 rows x chunk) into one of the S buffers
+//   PV warp         O += P . V, P read from tensor memory
 //   softmax warps   two threads per row, half a chunk's columns each: scores out of
 //                   tensor memory, running maximum and sum, P back over the scores
 //
-// A step is (query tile, chunk): S buffer of a step = its parity, so one step's
-// softmax runs under the other's products.  A two-tile unit takes both tiles
-// through each chunk; a one-tile unit alternates its even and odd chunks between
-// the two accumulators, which leave two partials per row.  At D = 256 there is one
-// accumulator (256 of the 512 columns), one softmax group, and still two S buffers.
+// A step is (query tile, chunk); step n of the CTA uses S buffer n % NBUF and is the
+// buffer's use n / NBUF, which gives every barrier's phase.  A two-tile unit takes both
+// tiles through each chunk, a tile per accumulator; a one-tile unit alternates its
+// even and odd chunks between the accumulators, which leave two partials per row.
+// At D = 256 there is one accumulator (256 of the 512 columns) and one softmax group.
 //
-// The P of a step overlays its S: PV(j) is issued before QK(j + 2), and the tensor
-// core runs one thread's products in order, so a QK never overwrites a P that is
-// still to be read.
+// The P of a step overlays its S, so QK(n + NBUF) waits for PV(n).  The products are
+// issued by two warps because between two of them a warp spends about as long on its
+// waits and counters as the tensor core on a product: from one warp a step (one
+// tile, 128 tokens, D = 128) took 2290 cycles, of which the products' issue was 1165.
 template <int D>
 struct SharedCfg {
-  static constexpr int CT = shared_chunk(D), NACC = shared_accs(D), CB = D / 64;
+  static constexpr int CT = shared_chunk(D), NBUF = 256 / CT, NACC = shared_accs(D), CB = D / 64;
   static constexpr int QR = shared_rows(D);
   static constexpr uint32_t kSlot = CT * D * 2;         // bytes of a K or V chunk
-  static constexpr uint32_t kBlock = CT * 128;          // one column block of it
+  // A chunk's rows lie in groups of 8, a group's 128-byte column blocks one after
+  // another: a page arrives with one copy, and the groups keep one stride.
+  static constexpr uint32_t kGroup = CB * 1024;
   static constexpr uint32_t kQBlock = QR * 128;         // one column block of q
   static constexpr uint32_t kQ = CB * kQBlock;
   // Ring slots: what is left beside q.  V's slots are held longer, from the copy
@@ -105,19 +160,19 @@ struct SharedCfg {
   static constexpr int kQueue = 4;
   static constexpr int kGroupWarps = 8;                 // a softmax group: 4 x 32 rows, two halves of the columns
   static constexpr int kSoftmaxWarps = kGroupWarps * NACC;
-  static constexpr int kCopyKWarp = kSoftmaxWarps, kCopyVWarp = kSoftmaxWarps + 1, kMmaWarp = kSoftmaxWarps + 2,
-                       kScheduleWarp = kSoftmaxWarps + 3;
+  static constexpr int kKWarp = kSoftmaxWarps, kVWarp = kSoftmaxWarps + 1, kQkWarp = kSoftmaxWarps + 2,
+                       kPvWarp = kSoftmaxWarps + 3;
   static constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
   static constexpr uint32_t ring = kQ, queue = ring + NS * kSlot, bars = queue + kQueue * 64;
   static constexpr uint32_t total = bars + 512 + 1024 /* alignment slack */;
-  static constexpr uint32_t kSCol = 128, kOCol = 256;   // S buffers at 0 and 128, O behind them
+  static constexpr uint32_t kSCol = CT, kOCol = NBUF * CT;  // tensor memory: S buffers, then O
 };
 static_assert(sizeof(SharedUnit) <= 64, "queue entry");
 
 template <int D>
 __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(const __grid_constant__ SharedParams p) {
   using C = SharedCfg<D>;
-  constexpr int CT = C::CT, NACC = C::NACC, NS = C::NS, CB = C::CB;
+  constexpr int CT = C::CT, NACC = C::NACC, NBUF = C::NBUF, NS = C::NS, CB = C::CB;
   static_assert(C::total <= (uint32_t)kSmemBudget, "shared-memory plan over budget");
   static_assert(C::kOCol + NACC * D <= 512, "tensor memory");
   extern __shared__ uint8_t smem_raw[];
@@ -127,9 +182,10 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::bars);
   const uint32_t bar0 = smem_addr(bars);
   const uint32_t full = bar0, empty = full + 8 * NS, q_full = empty + 8 * NS, q_empty = q_full + 16,
-                 s_full = q_empty + 16, p_full = s_full + 16, pv_done = p_full + 16, o_free = pv_done + 16,
+                 s_full = q_empty + 16, p_full = s_full + 8 * NBUF, pv_done = p_full + 8 * NBUF,
+                 o_free = pv_done + 8 * NBUF,
                  u_full = o_free + 16, u_empty = u_full + 8 * C::kQueue, idle = u_empty + 8 * C::kQueue;
-  constexpr int kBars = 2 * NS + 12 + 2 * C::kQueue + 1;
+  constexpr int kBars = 2 * NS + 3 * NBUF + 6 + 2 * C::kQueue + 1;
   static_assert(kBars * 8 + 8 <= 512, "barrier area");
   uint32_t *words = reinterpret_cast<uint32_t *>(bars + kBars);  // [0] tmem, [1] abort
   volatile int *abort_flag = reinterpret_cast<volatile int *>(words + 1);
@@ -143,16 +199,18 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + 8 * i, 1);
       mbar_init(q_empty + 8 * i, 1);
+      mbar_init(o_free + 8 * i, C::kGroupWarps);
+    }
+    for (int i = 0; i < NBUF; ++i) {
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_full + 8 * i, C::kGroupWarps);
       mbar_init(pv_done + 8 * i, 1);
-      mbar_init(o_free + 8 * i, C::kGroupWarps);
     }
     for (int i = 0; i < C::kQueue; ++i) {
       mbar_init(u_full + 8 * i, 1);
       mbar_init(u_empty + 8 * i, C::kSoftmaxWarps + 3);  // every role's warps
     }
-    mbar_init(idle, 1);
+    mbar_init(idle, 2);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -182,9 +240,72 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
   // rows, else each half in turn (one at D = 256).
   auto q_box_rows = [&](const SharedUnit &u) { return p.gt * (u.rest ? 1 : p.nseq); };
 
-  if (warp == C::kScheduleWarp) {
-    int k = 0;
-    bool ok = true;
+  // One ring's chunks of a unit, by a whole warp: K's or V's.
+  uint32_t slot = 0, phase = 1, used = 0;  // a first filling's wait passes at once
+  auto copy_chunks = [&](const SharedUnit &u, const CUtensorMap *map, uint32_t first_slot, uint32_t slots) -> bool {
+    const int32_t *table = u.rest ? p.tables + u.b0 * p.table_stride : p.shared_table;
+    const int box_log2 = p.box_log2, nbox = CT >> box_log2;
+    // Block of box 32 w + lane of a chunk: num_blocks (reads as zeros) behind the
+    // unit's tokens and for an id that is not one.
+    auto fetch = [&](int c, int w) -> int {
+      const int t = u.tok0 + c * CT + ((32 * w + lane) << box_log2);
+      if (c >= u.chunks || 32 * w + lane >= nbox || t >= u.tok1) return p.num_blocks;
+      const int id = __ldg(table + (t >> p.bs_log2));
+      if ((unsigned)id < (unsigned)p.num_blocks) return id;
+      atomicOr(p.err, kErrBlockId);
+      return p.num_blocks;
+    };
+    int id_next = fetch(0, 0);
+    for (int c = 0; c < u.chunks; ++c) {
+      int id = id_next;
+      id_next = fetch(c + 1, 0);  // a chunk ahead: the table's latency is not in the copies' way
+      const uint32_t bar = full + 8 * (first_slot + slot), dst = sring + (first_slot + slot) * C::kSlot;
+      if (!__all_sync(0xffffffffu, wait(empty + 8 * (first_slot + slot), phase))) return false;
+      const bool one = tc::elect();
+      if (one) mbar_arrive_expect_tx(bar, C::kSlot);
+      // a box's first row inside its page: only pages larger than a box have several
+      const int in_page = (u.tok0 + c * CT) & ((1 << p.bs_log2) - 1);
+#pragma unroll 1
+      for (int w = 0; 32 * w < nbox; ++w) {
+        if (w > 0) id = fetch(c, w);  // (pages of 1 and 2 tokens)
+#pragma unroll 1
+        for (int jj = 0; jj < 32 && 32 * w + jj < nbox; ++jj) {
+          const int j = 32 * w + jj, blk = __shfl_sync(0xffffffffu, id, jj), row = j << box_log2;
+          const int at = box_log2 < p.bs_log2 ? (in_page + row) & ((1 << p.bs_log2) - 1) : 0;
+          const uint32_t to = dst + (row >> 3) * C::kGroup + (row & 7) * 128;
+          if (one) {
+            if (p.box_kind == kBoxPage) {  // a page, or a chunk's worth of a larger one
+              tma_load_5d(to, map, 0, 0, 0, at >> 3, blk * p.blk_heads + u.kvh, bar);
+            } else if (p.box_kind == kBoxGroup) {  // 8 rows
+              tma_load_5d(to, map, 0, at, 0, u.kvh, blk, bar);
+            } else {  // pages below 8 tokens: a column block of a page
+#pragma unroll
+              for (int cb = 0; cb < CB; ++cb) tma_load_5d(to + cb * 1024, map, 0, 0, cb, u.kvh, blk, bar);
+            }
+          }
+        }
+      }
+      __syncwarp();
+      ++used;
+      if (++slot == slots) {
+        slot = 0;
+        phase ^= 1;
+      }
+    }
+    return true;
+  };
+  // Leaves no copy in flight, whoever gives up: a chunk is copied once its slot's
+  // earlier one has been read, so only a ring's last round can be open.
+  auto drain = [&](uint32_t first_slot, uint32_t slots) {
+    if (lane == 0)
+      for (uint32_t i = used > slots ? used - slots : 0; i < used; ++i)
+        wait(full + 8 * (first_slot + i % slots), (i / slots) & 1, true);
+  };
+
+  if (warp == C::kKWarp) {
+    uint32_t qphase = 3;  // a bit per half of q
+    int k = 0, half = 0;
+    bool ok = true, q_used[2] = {false, false};
     auto put = [&](const SharedUnit &u) {
       const int e = k % C::kQueue;
       ok = ok && (k < C::kQueue || __all_sync(0xffffffffu, wait(u_empty + 8 * e, (k / C::kQueue - 1) & 1)));
@@ -194,221 +315,143 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
       }
       ++k;
     };
-    shared_walk<D>(p, blockIdx.x, blockIdx.x == 0 ? p.cum : nullptr, put);
-    SharedUnit end{};
-    put(end);
-  } else if (warp == C::kCopyKWarp || warp == C::kCopyVWarp) {
-    const bool is_k = warp == C::kCopyKWarp;
-    const CUtensorMap *map = is_k ? &p.tmk : &p.tmv;
-    const int box_log2 = min(p.bs_log2, CT == 128 ? 7 : 6), box = 1 << box_log2, nbox = CT >> box_log2;
-    const int slot_mask = (1 << p.bs_log2) - 1;
-    const int first_slot = is_k ? 0 : C::NK, slots = is_k ? C::NK : C::NV;
-    uint32_t item = 0;               // chunks copied
-    uint32_t qn[2] = {0, 0};         // uses of each half of q
-    int half = 0;
+    shared_walk<D>(p, blockIdx.x, blockIdx.x == 0 ? p.cum : nullptr, [&](const SharedUnit &u) {
+      put(u);
+      const int box_rows = q_box_rows(u);
+      const bool both = NACC == 2 && box_rows > kTileRows;
+      const int h = both || NACC == 1 ? 0 : half;
+      if (!both && NACC == 2) half ^= 1;
+      ok = ok && __all_sync(0xffffffffu, wait(q_empty + 8 * h, qphase >> h & 1));
+      if (both) ok = ok && __all_sync(0xffffffffu, wait(q_empty + 8, qphase >> 1));
+      if (!ok) return;
+      if (tc::elect()) {
+        mbar_arrive_expect_tx(q_full + 8 * h, (uint32_t)box_rows * 128 * CB);
+        if (both) tc::arrive(q_full + 8);
+        for (int cb = 0; cb < CB; ++cb)
+          tma_load_4d(sq + cb * C::kQBlock + h * (kTileRows * 128), u.rest ? &p.tmqr : &p.tmqp, 0,
+                      u.kvh * p.g + u.ht * p.gt, cb, u.b0, q_full + 8 * h);
+      }
+      __syncwarp();
+      qphase ^= both ? 3 : 1 << h;
+      q_used[h] = true;
+      ok = copy_chunks(u, &p.tmk, 0, C::NK);
+    });
+    put(SharedUnit{});  // chunks == 0: the end
+    drain(0, C::NK);
+    if (lane == 0)
+      for (int h = 0; h < 2; ++h)
+        if (q_used[h]) wait(q_full + 8 * h, qphase >> h & 1, true);
+  } else if (warp == C::kVWarp) {
     bool ok = true;
     SharedUnit u;
-    for (int k = 0; ok && (ok = next_unit(k, u)) && u.chunks > 0; ++k) {
-      const int32_t *table = u.rest ? p.tables + u.b0 * p.table_stride : p.shared_table;
-      // Block of each box of a chunk, box j's in lane j % 32: num_blocks (reads as
-      // zeros) behind the unit's tokens and for an id that is not one.  Fetched a
-      // chunk ahead, so that the table's latency is not in the copies' way.
-      int ids[CT / 32];
-      auto fetch = [&](int c) {
-#pragma unroll
-        for (int w = 0; w < CT / 32; ++w) {
-          const int t = u.tok0 + c * CT + ((32 * w + lane) << box_log2);
-          ids[w] = p.num_blocks;
-          if (32 * w < nbox && 32 * w + lane < nbox && t < u.tok1) {
-            const int id = __ldg(table + (t >> p.bs_log2));
-            if ((unsigned)id < (unsigned)p.num_blocks) ids[w] = id;
-            else atomicOr(p.err, kErrBlockId);
-          }
-        }
-      };
-      fetch(0);
-      if (is_k) {  // ---- q
-        const int box_rows = q_box_rows(u);
-        const bool both = NACC == 2 && box_rows > kTileRows;
-        const int h = both || NACC == 1 ? 0 : half;
-        if (!both && NACC == 2) half ^= 1;
-        ok = qn[h] == 0 || __all_sync(0xffffffffu, wait(q_empty + 8 * h, (qn[h] - 1) & 1));
-        if (both) ok = ok && (qn[1] == 0 || __all_sync(0xffffffffu, wait(q_empty + 8, (qn[1] - 1) & 1)));
-        if (!ok) break;
-        if (tc::elect()) {
-          mbar_arrive_expect_tx(q_full + 8 * h, (uint32_t)box_rows * 128 * CB);
-          if (both) tc::arrive(q_full + 8);
-          for (int cb = 0; cb < CB; ++cb)
-            tma_load_4d(sq + cb * C::kQBlock + h * (kTileRows * 128), u.rest ? &p.tmqr : &p.tmqp, 0,
-                        u.kvh * p.g + u.ht * p.gt, cb, u.b0, q_full + 8 * h);
-        }
-        __syncwarp();
-        ++qn[h];
-        if (both) ++qn[1];
-      }
-      // ---- this warp's chunks
-      for (int c = 0; ok && c < u.chunks; ++c) {
-        const int slot = first_slot + item % slots;
-        if (item >= slots && !__all_sync(0xffffffffu, wait(empty + 8 * slot, (item / slots - 1) & 1))) {
-          ok = false;
-          break;
-        }
-        const uint32_t bar = full + 8 * slot, dst = sring + slot * C::kSlot;
-        const int tb = u.tok0 + c * CT;
-        // V's box that a sequence ends in: row by row, so that the slots behind the
-        // sequence are zeros, whatever they hold (a weight of 0 times NaN is NaN)
-        const int part = !is_k && u.tok1 < tb + CT && (u.tok1 & (box - 1)) != 0 ? (u.tok1 - tb) >> box_log2 : -1;
-        const bool one = tc::elect();
-        if (one) mbar_arrive_expect_tx(bar, C::kSlot);
-#pragma unroll
-        for (int w = 0; w < CT / 32; ++w) {
-#pragma unroll 1
-          for (int jj = 0; jj < 32 && 32 * w + jj < nbox; ++jj) {
-            const int j = 32 * w + jj, id = __shfl_sync(0xffffffffu, ids[w], jj);
-            const uint32_t to = dst + ((uint32_t)j << (box_log2 + 7));
-            if (j == part) {
-              for (int i = 0; i < box; ++i)
-                if (one)
-#pragma unroll
-                  for (int cb = 0; cb < CB; ++cb)
-                    tma_load_5d(to + cb * C::kBlock + i * 128, &p.tmv1, 0, (tb + (j << box_log2) + i) & slot_mask, cb,
-                                u.kvh, tb + (j << box_log2) + i < u.tok1 ? id : p.num_blocks, bar);
-            } else if (one) {
-#pragma unroll
-              for (int cb = 0; cb < CB; ++cb)
-                tma_load_5d(to + cb * C::kBlock, map, 0, (tb + (j << box_log2)) & slot_mask, cb, u.kvh, id, bar);
-            }
-          }
-        }
-        __syncwarp();
-        ++item;
-        if (c + 1 < u.chunks) fetch(c + 1);
-      }
-    }
-    // Leave no copy in flight, whoever gives up: a chunk is copied once its slot's
-    // earlier one has been read, so only the last `slots` can be open.
-    if (lane == 0) {
-      for (uint32_t i = item > (uint32_t)slots ? item - slots : 0; i < item; ++i)
-        wait(full + 8 * (first_slot + i % slots), (i / slots) & 1, true);
-      for (int h = 0; h < 2; ++h)
-        if (qn[h] > 0) wait(q_full + 8 * h, (qn[h] - 1) & 1, true);
-    }
-  } else if (warp == C::kMmaWarp) {
-    constexpr uint32_t IQK = tc::idesc(CT, false, false), IPV = tc::idesc(D, true, false);
-    // Two cursors over the CTA's steps, the score product's up to two steps ahead
-    // of the value product's (there are two S buffers), across units.
-    struct Cursor {
-      int k, j, steps, chunks, h;   // next unit of the queue; step of the unit; its q half
-      uint32_t item, step;          // chunks and steps of the units before it
-      bool two, both;
-    };
-    Cursor cq{-1, 0, 0, 0, 0, 0, 0, false, false}, cp = cq;
-    uint32_t qn[2] = {0, 0}, pn[2] = {0, 0}, on[2] = {0, 0};
+    for (int k = 0; ok && (ok = next_unit(k, u)) && u.chunks > 0; ++k) ok = copy_chunks(u, &p.tmv, C::NK, C::NV);
+    drain(C::NK, C::NV);
+  } else if (warp == C::kQkWarp) {
+    const uint32_t idesc = tc::idesc(CT, false, false) | (p.scale_log2 < 0.f ? tc::kNegateA : 0u);
+    const uint64_t qd0 = tc::smem_desc(sq, 16, 1024), kd0 = tc::smem_desc(sring, 16, C::kGroup);
+    uint32_t kslot = 0, kphase = 0, n = 0;  // ring slot and its phase, steps so far
+    uint32_t qphase = 0;                    // a bit per half of q
     int half = 0;
-    bool ok = true, more = true;
+    bool ok = true;
     auto all = [&](bool v) { return __all_sync(0xffffffffu, v) != 0; };
     SharedUnit u;
-    int queued_steps[2], queued_chunks[2];  // the units between the cursors: at most two, by parity
-    bool queued_two[2];
-    // The score product's cursor on its next step; false: no unit left (or gave up).
-    auto next_qk = [&]() -> bool {
-      if (cq.j < cq.steps) return true;
-      if (!more) return false;
-      cq.item += cq.chunks;
-      cq.step += cq.steps;
-      ++cq.k;
-      ok = next_unit(cq.k, u);
-      if (!ok || u.chunks == 0) {
-        more = false;
-        cq.steps = cq.chunks = cq.j = 0;
-        return false;
-      }
-      cq.two = NACC == 2 && u.rows > kTileRows;
-      cq.both = NACC == 2 && q_box_rows(u) > kTileRows;
-      cq.h = cq.both || NACC == 1 ? 0 : half;
-      if (!cq.both && NACC == 2) half ^= 1;
-      cq.chunks = u.chunks;
-      cq.steps = cq.two ? 2 * u.chunks : u.chunks;
-      cq.j = 0;
-      queued_steps[cq.k & 1] = cq.steps;
-      queued_chunks[cq.k & 1] = cq.chunks;
-      queued_two[cq.k & 1] = cq.two;
-      ok = all(wait(q_full + 8 * cq.h, qn[cq.h] & 1)) && (!cq.both || all(wait(q_full + 8, qn[1] & 1)));
-      ++qn[cq.h];
-      if (cq.both) ++qn[1];
-      return ok;
-    };
-    auto qk = [&]() -> bool {
-      const int c = cq.two ? cq.j >> 1 : cq.j, tile = cq.two ? cq.j & 1 : 0, buf = (cq.step + cq.j) & 1;
-      const uint32_t it = cq.item + c, slot = it % C::NK;
-      if (!all(wait(full + 8 * slot, (it / C::NK) & 1))) return false;
-      tc::fence_after();
-      const uint64_t qd = tc::smem_desc(sq + (cq.h + tile) * (kTileRows * 128), 16, 1024);
-      const uint64_t kd = tc::smem_desc(sring + slot * C::kSlot, 16, 1024);
-      if (tc::elect()) {
+    for (int k = 0; ok && (ok = next_unit(k, u)) && u.chunks > 0; ++k) {
+      const bool two = NACC == 2 && u.rows > kTileRows, both = NACC == 2 && q_box_rows(u) > kTileRows;
+      const int h = both || NACC == 1 ? 0 : half;
+      if (!both && NACC == 2) half ^= 1;
+      ok = all(wait(q_full + 8 * h, qphase >> h & 1)) && (!both || all(wait(q_full + 8, qphase >> 1)));
+      qphase ^= both ? 3 : 1 << h;
+      const uint64_t qd = qd0 + (uint32_t)h * (kTileRows * 128 >> 4);
+      auto step = [&](int tile, bool last_tile, bool last) -> bool {
+        const uint32_t buf = n % NBUF;
+        if (n >= NBUF && !all(wait(pv_done + 8 * buf, (n / NBUF - 1) & 1))) return false;
+        tc::fence_after();
+        const uint64_t a = qd + (uint32_t)tile * (kTileRows * 128 >> 4), b = kd0 + kslot * (C::kSlot >> 4);
+        const uint32_t d = tmem + buf * C::kSCol;
+        if (tc::elect()) {
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc::mma_ss(tmem + buf * C::kSCol, qd + (((kk >> 2) * C::kQBlock + (kk & 3) * 32) >> 4),
-                     kd + (((kk >> 2) * C::kBlock + (kk & 3) * 32) >> 4), IQK, kk > 0);
-        tc::commit(s_full + 8 * buf);
-        if (!cq.two || tile == 1) tc::commit(empty + 8 * slot);
-        if (cq.j == cq.steps - 1) {
-          tc::commit(q_empty + 8 * cq.h);
-          if (cq.both) tc::commit(q_empty + 8);
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::mma_ss(d, a + (((kk >> 2) * C::kQBlock + (kk & 3) * 32) >> 4),
+                       b + (((kk >> 2) * 1024 + (kk & 3) * 32) >> 4), idesc, kk > 0);
+          tc::commit(s_full + 8 * buf);
+          if (last_tile) tc::commit(empty + 8 * kslot);
+          if (last) {
+            tc::commit(q_empty + 8 * h);
+            if (both) tc::commit(q_empty + 8);
+          }
+        }
+        __syncwarp();
+        ++n;
+        return true;
+      };
+      for (int c = 0; ok && c < u.chunks; ++c) {
+        ok = all(wait(full + 8 * kslot, kphase)) && step(0, !two, !two && c + 1 == u.chunks) &&
+             (!two || step(1, true, c + 1 == u.chunks));
+        if (++kslot == C::NK) {
+          kslot = 0;
+          kphase ^= 1;
         }
       }
-      __syncwarp();
-      ++cq.j;
-      return true;
-    };
-    auto pv = [&]() -> bool {
-      if (cp.j == cp.steps) {  // on to the next unit, which the other cursor has been given
-        cp.item += cp.chunks;
-        cp.step += cp.steps;
-        ++cp.k;
-        cp.steps = queued_steps[cp.k & 1];
-        cp.chunks = queued_chunks[cp.k & 1];
-        cp.two = queued_two[cp.k & 1];
-        cp.j = 0;
-      }
-      const int c = cp.two ? cp.j >> 1 : cp.j, buf = (cp.step + cp.j) & 1, acc = NACC == 2 ? buf : 0;
-      const bool first = cp.j < NACC;
-      const uint32_t it = cp.item + c, slot = C::NK + it % C::NV;
-      if (first) {  // the last unit's sums have been read
-        if (on[acc] > 0 && !all(wait(o_free + 8 * acc, (on[acc] - 1) & 1))) return false;
-        ++on[acc];
-      }
-      if (!all(wait(full + 8 * slot, (it / C::NV) & 1))) return false;
-      if (!all(wait(p_full + 8 * buf, pn[buf] & 1))) return false;
-      ++pn[buf];
-      tc::fence_after();
-      const uint64_t vd = tc::smem_desc(sring + slot * C::kSlot, C::kBlock, 1024);
-      if (tc::elect()) {
-#pragma unroll
-        for (int kk = 0; kk < CT / 16; ++kk)
-          tc::mma_ts(tmem + C::kOCol + acc * D, tmem + buf * C::kSCol + kk * 8, vd + (kk * 2048 >> 4), IPV,
-                     !first || kk > 0);
-        tc::commit(pv_done + 8 * acc);
-        if (!cp.two || (cp.j & 1)) tc::commit(empty + 8 * slot);
-      }
-      __syncwarp();
-      ++cp.j;
-      return true;
-    };
-    int ahead = 0;
-    while (ok) {
-      while (ok && ahead < 2 && next_qk()) {
-        ok = qk();
-        ++ahead;
-      }
-      if (!ok || ahead == 0) break;
-      ok = pv();
-      --ahead;
     }
     if (tc::elect()) tc::commit(idle);  // every product issued above has completed when this arrives
+  } else if (warp == C::kPvWarp) {
+    constexpr uint32_t idesc = tc::idesc(D, true, false);
+    const uint64_t vd0 = tc::smem_desc(sring + C::NK * C::kSlot, 1024, C::kGroup);
+    uint32_t vslot = 0, vphase = 0, n = 0;
+    uint32_t ophase = 3;  // a bit per accumulator; the first wait on each passes at once
+    bool ok = true;
+    auto all = [&](bool v) { return __all_sync(0xffffffffu, v) != 0; };
+    SharedUnit u;
+    for (int k = 0; ok && (ok = next_unit(k, u)) && u.chunks > 0; ++k) {
+      const bool two = NACC == 2 && u.rows > kTileRows;
+      auto step = [&](bool first, bool last_tile) -> bool {
+        const uint32_t buf = n % NBUF, acc = NACC == 2 ? n & 1 : 0;
+        if (first) {  // the last unit's sums have been read
+          if (!all(wait(o_free + 8 * acc, ophase >> acc & 1))) return false;
+          ophase ^= 1 << acc;
+        }
+        if (!all(wait(p_full + 8 * buf, n / NBUF & 1))) return false;
+        tc::fence_after();
+        const uint64_t b = vd0 + vslot * (C::kSlot >> 4);
+        const uint32_t d = tmem + C::kOCol + acc * D, a = tmem + buf * C::kSCol;
+        if (tc::elect()) {
+#pragma unroll
+          for (int kk = 0; kk < CT / 16; ++kk) tc::mma_ts(d, a + kk * 8, b + (kk * 2 * C::kGroup >> 4), idesc, !first || kk > 0);
+          tc::commit(pv_done + 8 * buf);
+          if (last_tile) tc::commit(empty + 8 * (C::NK + vslot));
+        }
+        __syncwarp();
+        ++n;
+        return true;
+      };
+      for (int c = 0; ok && c < u.chunks; ++c) {
+        ok = all(wait(full + 8 * (C::NK + vslot), vphase));
+        const int nv = u.tok1 - (u.tok0 + c * CT), bs = 1 << p.bs_log2;
+        if (ok && nv < CT && (u.tok1 & (bs - 1)) != 0) {
+          // The page the sequence ends in arrived whole: zeros over the slots behind
+          // the sequence, whatever they hold (a weight of 0 times NaN is NaN).
+          const int end = min(CT, nv + bs - (u.tok1 & (bs - 1)));
+          uint8_t *v = smem + C::ring + (C::NK + vslot) * C::kSlot;
+          for (int x = lane; x < (end - nv) * (D / 8); x += 32) {
+            const int row = nv + x / (D / 8), at = x % (D / 8) * 16;  // (the swizzle stays inside the 128 bytes)
+            *reinterpret_cast<uint4 *>(v + (row >> 3) * C::kGroup + (at >> 7) * 1024 + (row & 7) * 128 + (at & 127)) =
+                make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        ok = ok && step(two ? c == 0 : c < NACC, !two) && (!two || step(c == 0, true));
+        if (++vslot == C::NV) {
+          vslot = 0;
+          vphase ^= 1;
+        }
+      }
+    }
+    if (tc::elect()) tc::commit(idle);
   } else {
     // ---- softmax: a row's columns in two halves, one thread each
     constexpr int HC = CT / 2;
+    constexpr int kExpFma = 1, kExpOf = 4;  // of each four pairs, one on the FMA pipe: ex2 alone is 16 a cycle
     const int w = warp / C::kGroupWarps, half = warp >> 2 & 1, wq = warp & 3, row_in_tile = wq * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
     const uint32_t ocol = lanes + C::kOCol + w * D + half * (D / 2);
@@ -422,11 +465,18 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
       tc::fence_after();
       return tc::ld1(other);
     };
-    const float sl2 = p.scale_log2;
-    const float none = sl2 >= 0.f ? -INFINITY : INFINITY;  // below every score
+    // Barrier of the two warps that also ORs a value over them.
+    auto any_of_both = [&](bool v) -> bool {
+      uint32_t r;
+      asm volatile(
+          "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.red.or.pred q, %2, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+          : "=r"(r)
+          : "r"((uint32_t)v), "r"(1 + w * 4 + wq)
+          : "memory");
+      return r != 0;
+    };
+    const float sl2 = fabsf(p.scale_log2);  // a negative scale's sign is in the score product
     uint32_t step = 0;               // steps of all units so far
-    uint32_t sn[2] = {0, 0};         // S buffer uses
-    uint32_t vn = 0;                 // products into this group's accumulator
     bool ok = true;
     SharedUnit u;
     for (int k = 0; ok && (ok = next_unit(k, u)) && u.chunks > 0; ++k) {
@@ -438,9 +488,8 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
       const bool live = tile * kTileRows + wq * 32 < u.rows;  // the warp has a row
       float m = -INFINITY, l = 0.f;
       for (int j = j0; ok && j < steps; j += NACC) {
-        const int buf = (int)(step + j) & 1;
-        ok = __all_sync(0xffffffffu, wait(s_full + 8 * buf, sn[buf] & 1));
-        ++sn[buf];
+        const uint32_t buf = (step + j) % NBUF;
+        ok = __all_sync(0xffffffffu, wait(s_full + 8 * buf, (step + j) / NBUF & 1));
         if (!ok) break;
         if (live) {
           tc::fence_after();
@@ -453,33 +502,26 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
           if (nv < HC) {
 #pragma unroll
             for (int i = 0; i < HC; ++i)
-              if (i >= nv) s[i] = none;
+              if (i >= nv) s[i] = -INFINITY;
           }
-          float mx[4] = {none, none, none, none};
-          if (sl2 >= 0.f) {
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < HC; i += 2) mx[i >> 1 & 3] = fmaxf(mx[i >> 1 & 3], fmaxf(s[i], s[i + 1]));
-            mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          } else {
-#pragma unroll
-            for (int i = 0; i < HC; i += 2) mx[i >> 1 & 3] = fminf(mx[i >> 1 & 3], fminf(s[i], s[i + 1]));
-            mx[0] = fminf(fminf(mx[0], mx[1]), fminf(mx[2], mx[3]));
-          }
-          // Each half's maximum travels in its last column of S, which it has read.
-          // Behind the exchange all of S has been read: P, in its first half, may
-          // overwrite it.
-          float top = mx[0] * sl2;
-          top = fmaxf(top, exchange(scol + half * HC + HC - 1, scol + (half ^ 1) * HC + HC - 1, top));
+          for (int i = 0; i < HC; i += 2) mx[i >> 1 & 3] = fmaxf(fmaxf(mx[i >> 1 & 3], s[i]), s[i + 1]);
+          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
           // The reference moves only when a score passes it by 2^8: any
           // reference gives the same result as long as l and O share it, and the
-          // rescale of O is skipped on almost every chunk.
-          if (__any_sync(0xffffffffu, top > m + 8.f)) {
+          // exchange of the halves' maxima and the rescale of O are skipped on
+          // almost every chunk.  Behind this barrier both halves of S have been
+          // read: P, in its first half, may overwrite it.
+          if (any_of_both(top > m + 8.f)) {
+            top = fmaxf(top, exchange(scol + half * HC + HC - 1, scol + (half ^ 1) * HC + HC - 1, top));
             const float mn = fmaxf(m, top);
             const float a = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
             m = mn;
             l *= a;
             if (j != j0) {  // O holds the earlier chunks once their product is done
-              ok = __all_sync(0xffffffffu, wait(pv_done + 8 * w, (vn - 1) & 1));
+              const uint32_t n = step + j - NACC;  // the group's step before this one
+              ok = __all_sync(0xffffffffu, wait(pv_done + 8 * (n % NBUF), n / NBUF & 1));
               if (!ok) break;
               tc::fence_after();
 #pragma unroll 1
@@ -494,33 +536,39 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
             }
           }
           const float ref = m == -INFINITY ? 0.f : m;
-          float ls[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t scale = duo(sl2, sl2), shift = duo(-ref, -ref);
+          uint64_t ls[2] = {0, 0};
 #pragma unroll
           for (int i = 0; i < HC; i += 32) {
             uint32_t pk[16];
 #pragma unroll
             for (int x = 0; x < 32; x += 2) {
-              const float e0 = fast_exp2(s[i + x] * sl2 - ref), e1 = fast_exp2(s[i + x + 1] * sl2 - ref);
-              ls[x & 2] += e0;
-              ls[(x & 2) + 1] += e1;
-              pk[x / 2] = pack_bf16x2(e0, e1);
+              const uint64_t v = fma2(duo(s[i + x], s[i + x + 1]), scale, shift);
+              float2 e;
+              if (x / 2 % kExpOf < kExpFma) {
+                e = exp2_fma(v);
+              } else {
+                e = parts(v);
+                e.x = fast_exp2(e.x);
+                e.y = fast_exp2(e.y);
+              }
+              ls[x >> 1 & 1] = add2(ls[x >> 1 & 1], duo(e.x, e.y));
+              pk[x / 2] = pack_bf16x2(e.x, e.y);
             }
             tc::st16(scol + (half * HC + i) / 2, pk);
           }
-          l += (ls[0] + ls[1]) + (ls[2] + ls[3]);  // fp32 weights: rounded ones would move lse by up to 2^-9
+          const float2 l2 = parts(add2(ls[0], ls[1]));
+          l += l2.x + l2.y;  // fp32 weights: rounded ones would move lse by up to 2^-9
           if (j + NACC >= steps) l += exchange(scol + HC + half, scol + HC + (half ^ 1), l);  // the unit's sum
           tc::wait_st();
           tc::fence_before();
         }
-        ++vn;
         __syncwarp();
         if (lane == 0) tc::arrive(p_full + 8 * buf);
       }
       if (ok && steps > j0) {
-        // (a parity tells only neighbouring phases apart: with one accumulator the
-        // last two products may both be open)
-        if (NACC == 1 && steps > 1) ok = __all_sync(0xffffffffu, wait(pv_done + 8 * w, (vn - 2) & 1));
-        ok = ok && __all_sync(0xffffffffu, wait(pv_done + 8 * w, (vn - 1) & 1));
+        const uint32_t n = step + j0 + (steps - 1 - j0) / NACC * NACC;  // the group's last step
+        ok = __all_sync(0xffffffffu, wait(pv_done + 8 * (n % NBUF), n / NBUF & 1));
         if (ok && live) {
           tc::fence_after();
           const float inv = 1.f / l;

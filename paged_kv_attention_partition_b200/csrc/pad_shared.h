@@ -33,9 +33,17 @@ __host__ __device__ constexpr int shared_chunk(int D) { return D == 256 ? 64 : 1
 // Accumulators: two tiles of rows, or one tile's even and odd chunks.
 __host__ __device__ constexpr int shared_accs(int D) { return D == 256 ? 1 : 2; }
 
+// What one copy of K or V brings: rows of 128-byte column blocks, laid out in groups
+// of 8 rows x all column blocks.
+enum SharedBox : int32_t {
+  kBoxPage = 0,   // a page's rows (at most a chunk's): (128 bytes, 8 rows, column blocks, row groups, block and head)
+  kBoxGroup = 1,  // 8 rows: (128 bytes, 8 rows, column blocks, head, block), for caches whose block stride is not
+                  // a multiple of the head stride
+  kBoxRows = 2,   // pages below 8 slots: one column block of a page: (128 bytes, rows, column block, head, block)
+};
+
 struct SharedParams {
-  CUtensorMap tmk, tmv;    // caches, boxes of one 128-byte column block x a page (at most a chunk)
-  CUtensorMap tmv1;        // V with boxes of one slot
+  CUtensorMap tmk, tmv;    // caches, boxes as box_kind says
   CUtensorMap tmqp, tmqr;  // q: boxes of 64 head_dim x gt heads x nseq sequences (prefix), x 1 (rest)
   const uint16_t *q;
   int64_t q_sb, q_sh;
@@ -52,6 +60,8 @@ struct SharedParams {
   int32_t HT, gt;      // head tiles of a group, heads of one (the last may have fewer)
   int32_t nseq, nrb;   // sequences of a prefix row block, row blocks
   int32_t bs_log2;
+  int32_t box_kind, box_log2;  // SharedBox, rows of a box
+  int32_t blk_heads;           // kBoxPage: block stride / head stride
   int32_t ctas;
   int32_t w_item, w_pre1, w_pre2, w_rest;  // cost of an item; of a prefix chunk of one and two tiles, of a rest chunk
   float scale_log2, v_scale;

@@ -71,24 +71,53 @@ Layout layout(const Shape &s, int ctas, pad::SharedParams *p) {
   return l;
 }
 
-// A cache as (128 bytes of head_dim, slot, the rest of head_dim, kv head, block)
-// with boxes of one 128-byte column block x `box_rows` slots, 128-byte swizzle
-// (an E4M3 cache unswizzled: its codes are widened on the way to the operand).
-pad_status cache_map(CUtensorMap *map, const pad_tensor *t, int box_rows, const char *name) {
+// How a cache's pages are copied (SharedBox), K and V alike.
+void choose_box(const pad_tensor *k, const pad_tensor *v, int chunk, pad::SharedParams *p) {
+  const int64_t NB = k->shape[0], H = k->shape[1], bs = k->shape[2];
+  p->blk_heads = 1;
+  if (bs < 8) {
+    p->box_kind = pad::kBoxRows;
+    p->box_log2 = p->bs_log2;
+    return;
+  }
+  p->box_kind = pad::kBoxGroup;
+  p->box_log2 = 3;
+  // block and head as one coordinate, block * (block stride / head stride) + head
+  auto ratio = [&](const pad_tensor *t) -> int64_t {
+    if (NB == 1) return H;
+    if (H == 1) return 1;
+    return t->stride[1] > 0 && t->stride[0] % t->stride[1] == 0 ? t->stride[0] / t->stride[1] : 0;
+  };
+  const int64_t r = ratio(k);
+  if (r < H || r != ratio(v) || NB * r + H > 0x7fffffffll) return;  // (r >= H: block num_blocks is out of range)
+  p->box_kind = pad::kBoxPage;
+  p->blk_heads = (int32_t)r;
+  while ((1 << p->box_log2) < chunk && (1 << p->box_log2) < bs) ++p->box_log2;
+}
+
+// A bf16 cache's tensor map for the boxes of `p`, 128-byte swizzle.
+pad_status cache_map(CUtensorMap *map, const pad_tensor *t, const pad::SharedParams &p, const char *name) {
   pad::TensorMapEncodeFn enc = pad::host_tensor_map_encoder();
   if (enc == nullptr) return host_fail(PAD_ERR_CUDA, "the CUDA driver does not provide cuTensorMapEncodeTiled");
-  const bool fp8 = t->dtype == PAD_FP8_E4M3;
-  const int64_t eb = fp8 ? 1 : 2, rowb = t->shape[3] * eb, rw = fp8 ? rowb : 128;
-  auto bytes = [&](int i, int64_t natural) { return (cuuint64_t)(t->shape[i] > 1 ? t->stride[i] * eb : natural); };
-  const cuuint64_t dims[5] = {(cuuint64_t)(rw / eb), (cuuint64_t)t->shape[2], (cuuint64_t)(rowb / rw),
-                              (cuuint64_t)t->shape[1], (cuuint64_t)t->shape[0]};
-  const cuuint64_t strides[4] = {bytes(2, rowb), (cuuint64_t)rw, bytes(1, t->shape[2] * rowb),
-                                 bytes(0, t->shape[1] * t->shape[2] * rowb)};
-  const cuuint32_t box[5] = {(cuuint32_t)(rw / eb), (cuuint32_t)box_rows, 1, 1, 1}, one[5] = {1, 1, 1, 1, 1};
-  const CUresult r = enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, t->data, dims,
-                         strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         fp8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  const cuuint64_t NB = t->shape[0], H = t->shape[1], bs = t->shape[2], CB = t->shape[3] / 64;
+  auto bytes = [&](int i, int64_t natural) { return (cuuint64_t)(t->shape[i] > 1 ? t->stride[i] * 2 : natural); };
+  const cuuint64_t row = bytes(2, t->shape[3] * 2), head = bytes(1, bs * row), block = bytes(0, H * head);
+  const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  CUresult r;
+  if (p.box_kind == pad::kBoxPage) {
+    const cuuint64_t dims[5] = {64, 8, CB, bs / 8, (NB - 1) * p.blk_heads + H};
+    const cuuint64_t strides[4] = {row, 128, 8 * row, H > 1 ? head : block};
+    const cuuint32_t box[5] = {64, 8, (cuuint32_t)CB, (cuuint32_t)(1 << p.box_log2) / 8, 1};
+    r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, t->data, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  } else {
+    const cuuint64_t dims[5] = {64, bs, CB, H, NB};
+    const cuuint64_t strides[4] = {row, 128, head, block};
+    const cuuint32_t box[5] = {64, (cuuint32_t)(1 << p.box_log2), p.box_kind == pad::kBoxGroup ? (cuuint32_t)CB : 1, 1,
+                               1};
+    r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, t->data, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  }
   if (r != CUDA_SUCCESS)
     return host_fail(PAD_ERR_INVALID_ARG, "%s: strides/shape not expressible as a TMA tensor (cuTensorMapEncodeTiled %d)",
                      name, (int)r);
@@ -245,10 +274,11 @@ extern "C" pad_status pad_decode_shared(const pad_tensor *q, const pad_tensor *k
   } else if ((st = pad::host_scratch(device, stream, l.total, &workspace)) != PAD_OK) {
     return st;
   }
-  const int box = (int)(bs < pad::shared_chunk((int)D) ? bs : pad::shared_chunk((int)D));
-  if ((st = cache_map(&p.tmk, k_cache, box, "k_cache")) != PAD_OK) return st;
-  if ((st = cache_map(&p.tmv, v_cache, box, "v_cache")) != PAD_OK) return st;
-  if ((st = cache_map(&p.tmv1, v_cache, 1, "v_cache")) != PAD_OK) return st;
+  choose_box(k_cache, v_cache, pad::shared_chunk((int)D), &p);
+  if (!fp8) {
+    if ((st = cache_map(&p.tmk, k_cache, p, "k_cache")) != PAD_OK) return st;
+    if ((st = cache_map(&p.tmv, v_cache, p, "v_cache")) != PAD_OK) return st;
+  }
   if ((st = query_map(&p.tmqp, q, p.gt, p.nseq)) != PAD_OK) return st;
   if ((st = query_map(&p.tmqr, q, p.gt, 1)) != PAD_OK) return st;
   p.q = static_cast<const uint16_t *>(q->data);

@@ -115,6 +115,8 @@ __host__ __device__ constexpr uint32_t idesc(int n, bool b_mn_major, bool f16) {
          ((uint32_t)(n >> 3) << 17) | (8u << 24);
 }
 
+constexpr uint32_t kNegateA = 1u << 13;  // of the instruction descriptor: -A
+
 constexpr uint64_t kWaitNs = 1000000000ull;  // no wait can legitimately take 1 s
 
 // Waits for the phase of `bar` with this parity, at most kWaitNs; gives up at

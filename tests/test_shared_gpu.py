@@ -66,6 +66,29 @@ def test_matches_the_definition(cuda_device, name, kv):
 
 
 @pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("bs", [2, 8, 16, 256])
+@pytest.mark.parametrize("layout", ["heads outermost", "padded rows", "K and V unlike"])
+def test_cache_layouts(cuda_device, layout, bs, kv):
+    # block and head strides that make one coordinate and ones that do not
+    batch = Batch(4, 8, 2, 128, bs, max(1, 160 // bs), [0, 3, 200, 77], kv=kv, seed=bs)
+    a = batch.device(cuda_device)
+    for name in ("k_cache", "v_cache"):
+        c = a[name]
+        if layout == "heads outermost":
+            a[name] = c.transpose(0, 1).contiguous().transpose(0, 1)
+        elif layout == "padded rows":
+            wide = torch.zeros(*c.shape[:3], 160, dtype=torch.bfloat16, device=cuda_device).to(c.dtype)
+            wide.view(torch.uint8).fill_(0x7F)
+            wide[..., :128] = c
+            a[name] = wide[..., :128]
+        elif name == "v_cache":
+            a[name] = c.transpose(1, 2).contiguous().transpose(1, 2)
+    out, lse = pad.pad_decode_shared(**a, lse=True)
+    check(out, lse, batch.reference(), layout)
+    assert pad.pad_check_device_errors() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
 def test_same_as_pad_decode(cuda_device, kv):
     # what pad_decode gives for the same sequences, within both calls' tolerance
     batch = Batch(9, 16, 4, 128, 16, 20, [11 * i for i in range(9)], kv=kv, seed=4)
