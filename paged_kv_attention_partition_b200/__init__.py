@@ -17,8 +17,8 @@ Functions carry the C names: ``pad_decode``, ``pad_decode_with_workspace``,
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
-import struct
 from typing import Optional, Tuple, Union
 
 import torch
@@ -124,7 +124,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.pad_inject_stage_timeout.restype = ctypes.c_int
     lib.pad_release_workspace.argtypes = [ctypes.c_int32]
     lib.pad_release_workspace.restype = ctypes.c_int
-    # these three take descriptors packed by _Call: addresses, not PadTensor pointers
+    # (descriptors by address: these three are called through _pad_torch)
     V, F, I = ctypes.c_void_p, ctypes.c_float, ctypes.c_int32
     lib.pad_qk_norm_rope.argtypes = [V, V, V, V, F, V, V, I, V, V, V]
     lib.pad_qk_norm_rope.restype = ctypes.c_int
@@ -317,54 +317,43 @@ def pad_decode_with_workspace(q, k_cache, v_cache, block_tables, seq_lens, scale
     _raise(st)
 
 
-# pad_tensor of a tensor of 1 to 4 dims, and the two options structs that hold
-# descriptors' addresses (C layout, native alignment).
-_PACK = [None] + [struct.Struct(f"@Pii{n}q{8 * (4 - n)}x{n}q{8 * (4 - n)}x") for n in range(1, 5)]
-_PACK_APPEND = struct.Struct("@PixxxxPfxxxxPPPff")
-_PACK_DECODE = struct.Struct("@ixxxxPff")
+# The calls below go through _pad_torch.so (csrc/pad_torch.cpp), which packs the
+# descriptors and allocates the outputs: a decode step makes several of them per
+# layer, and marshalling them from here costs more than their launches.
+_fast = None
 
 
-class _Call:
-    """The descriptors of one call, packed into one buffer: a decode step makes
-    several such calls per layer, and a ctypes structure per tensor costs more
-    than the launch.  ``at(name, t)`` is the descriptor's address (None for None)
-    and checks that the tensor is on the call's device."""
+def _load_fast():
+    global _fast
+    if _fast is not None:
+        return _fast
+    path = os.path.join(_HERE, "_pad_torch.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with `python -m paged_kv_attention_partition_b200._build`")
+    lib = load_library()
+    spec = importlib.util.spec_from_file_location("_pad_torch", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                  for f in (lib.pad_qk_norm_rope, lib.pad_append_kv, lib.pad_decode_shared)))
+    _fast = module
+    return module
 
-    __slots__ = ("buf", "base", "used", "dev")
 
-    def __init__(self, dev: torch.device):
-        if dev.type != "cuda":
-            raise ValueError(f"expected CUDA tensors, got one on {dev}")
-        self.buf = bytearray(1280)
-        self.base = ctypes.addressof(ctypes.c_char.from_buffer(self.buf))
-        self.used = 0
-        self.dev = dev
-
-    def at(self, name: str, t: Optional[torch.Tensor]) -> Optional[int]:
-        if t is None:
-            return None
-        if t.device != self.dev:
-            raise ValueError(f"{name} is on {t.device}, expected {self.dev}")
-        dt = _DTYPES.get(t.dtype)
-        if dt is None:
-            raise TypeError(f"{name}: unsupported dtype {t.dtype}")
-        n = t.dim()
-        if not 1 <= n <= 4:
-            raise ValueError(f"{name}: 1 to 4 dims, got {n}")
-        return self.put(_PACK[n], t.data_ptr(), dt, n, *t.shape, *t.stride())
-
-    def put(self, layout: struct.Struct, *values) -> int:
-        at = self.used
-        layout.pack_into(self.buf, at, *values)
-        self.used = at + (layout.size + 7 & ~7)
-        return self.base + at
-
-    def run(self, fn, *args):
-        if self.dev.index == torch.cuda.current_device():
-            _raise(fn(*args))
-        else:
-            with torch.cuda.device(self.dev):
-                _raise(fn(*args))
+def _invoke(fn, first: torch.Tensor, stream, *args):
+    """``fn(*args, stream)`` on the device of ``first``; its outputs, or PadError."""
+    dev = first.device
+    if dev.type != "cuda":
+        raise ValueError(f"expected CUDA tensors, got one on {dev}")
+    handle = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream_handle(stream, dev)
+    if dev.index == torch.cuda.current_device():
+        r = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            r = fn(*args, handle)
+    if type(r) is int:
+        _raise(r)
+    return r
 
 
 def pad_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
@@ -378,17 +367,8 @@ def pad_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optio
     Without a weight that tensor is not normed; without ``inv_freq`` (fp32 [R/2],
     with ``positions`` int32 [T]) nothing is rotated; k may be None.  ``q_out`` /
     ``k_out`` receive the rows (they may be q and k themselves).  Returns (q_out, k_out)."""
-    c = _Call(q.device)
-    if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if k_out is None and k is not None:
-        k_out = torch.empty(k.shape, dtype=k.dtype, device=q.device)
-    args = (c.at("q", q), c.at("k", k), c.at("q_weight", q_weight), c.at("k_weight", k_weight), eps,
-            c.at("positions", positions), c.at("inv_freq", inv_freq), int(interleaved), c.at("q_out", q_out),
-            c.at("k_out", k_out))
-    if q.numel() > 0:  # no token: no data pointers either
-        c.run(load_library().pad_qk_norm_rope, *args, _stream_handle(stream, q.device))
-    return q_out, k_out
+    return _invoke((_fast or _load_fast()).qk_norm_rope, q, stream, q, k, q_weight, k_weight, positions, inv_freq, eps,
+                   interleaved, q_out, k_out)
 
 
 def pad_append_kv(k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, block_tables: torch.Tensor,
@@ -405,20 +385,8 @@ def pad_append_kv(k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, blo
     sequence t's).  ``q`` [T, Hq, D]: the tokens' query rows, normed and rotated by
     the same launch into ``q_out``.  An E4M3 cache holds x / ``k_scale``, x /
     ``v_scale``.  Returns q_out (None without q)."""
-    c = _Call(k.device)
-    if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    if q is None and q_out is not None:
-        raise ValueError("q_out without q")
-    at = c.at
-    args = (at("k", k), at("v", v), at("positions", positions), at("seq_ids", seq_ids),
-            at("block_tables", block_tables))
-    opts = c.put(_PACK_APPEND, at("inv_freq", inv_freq) or 0, int(interleaved), at("k_weight", k_weight) or 0, eps,
-                 at("q", q) or 0, at("q_weight", q_weight) or 0, at("q_out", q_out) or 0, k_scale, v_scale)
-    if k.numel() > 0:
-        c.run(load_library().pad_append_kv, *args, opts, at("k_cache", k_cache), at("v_cache", v_cache),
-              _stream_handle(stream, k.device))
-    return q_out
+    return _invoke((_fast or _load_fast()).append_kv, k, stream, k, v, positions, block_tables, k_cache, v_cache,
+                   seq_ids, inv_freq, interleaved, k_weight, eps, q, q_weight, q_out, k_scale, v_scale)
 
 
 def pad_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, shared_table: torch.Tensor,
@@ -432,24 +400,8 @@ def pad_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     least n * block_size.  ``workspace``: a contiguous tensor of at least
     ``pad_decode_shared_plan(...)["workspace_bytes"]`` bytes instead of the
     library's scratch.  Returns (out, lse)."""
-    c = _Call(q.device)
-    if out is None:
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    if lse is True:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-    elif lse is False:
-        lse = None
-    if workspace is not None and (workspace.device != q.device or not workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous tensor on q's device")
-    at = c.at
-    args = (at("q", q), at("k_cache", k_cache), at("v_cache", v_cache), at("shared_table", shared_table),
-            at("block_tables", block_tables), at("seq_lens", seq_lens), scale,
-            c.put(_PACK_DECODE, 0, at("sinks", sinks) or 0, k_scale, v_scale), at("out", out), at("lse", lse))
-    if q.numel() > 0:
-        c.run(load_library().pad_decode_shared, *args, workspace.data_ptr() if workspace is not None else None,
-              workspace.numel() * workspace.element_size() if workspace is not None else 0,
-              _stream_handle(stream, q.device))
-    return out, lse
+    return _invoke((_fast or _load_fast()).decode_shared, q, stream, q, k_cache, v_cache, shared_table, block_tables,
+                   seq_lens, scale, out, lse, sinks, k_scale, v_scale, workspace)
 
 
 def pad_decode_shared_plan(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, block_size: int,

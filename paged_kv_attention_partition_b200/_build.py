@@ -1,4 +1,5 @@
-"""Builds libpad.so in-tree with nvcc for sm_100a (cross-compiles without a GPU)."""
+"""Builds libpad.so in-tree with nvcc for sm_100a (cross-compiles without a GPU),
+and _pad_torch.so, the binding's argument marshalling, with g++."""
 from __future__ import annotations
 
 import glob
@@ -12,6 +13,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libpad.so")
+BINDING = os.path.join(PKG, "_pad_torch.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 SOURCES = ["pad_api.cpp", "pad_rows_api.cpp", "pad_shared_api.cpp", "pad_partition.cu", "pad_umma.cu", "pad_no_alloc.cu",
@@ -44,8 +46,36 @@ def compile_command(out: str, extra=()):
             "-I", INCLUDE, "-I", CSRC, *extra, "-o", out] + [os.path.join(CSRC, s) for s in SOURCES]
 
 
+def binding_command(out: str):
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], INCLUDE]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *(f"-I{d}" for d in inc), os.path.join(CSRC, "pad_torch.cpp"), "-o", out, f"-L{os.path.join(root, 'lib')}",
+            "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
+def build_binding(force: bool = False) -> str:
+    """Compile _pad_torch.so if its source or pad.h is newer (or force)."""
+    inputs = [os.path.join(CSRC, "pad_torch.cpp"), os.path.join(INCLUDE, "pad.h"), os.path.abspath(__file__)]
+    if not force and os.path.exists(BINDING) and all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in inputs):
+        return BINDING
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = binding_command(tmp)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libpad.so if any source is newer (or force)."""
+    """Compile libpad.so (and the binding's module) if any source is newer (or force)."""
+    build_binding(force)
     if not force and not is_stale():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"

@@ -1,6 +1,6 @@
 """pad_qk_norm_rope, pad_append_kv and pad_decode_shared without a GPU: every
 refusal comes before any device work, with a status and a message; the shared
-plan; the packed descriptors of the binding against the C structs."""
+plan; what the binding refuses by itself."""
 import ctypes
 
 import pytest
@@ -202,29 +202,15 @@ def test_shared_plan(lib):
         pad.pad_decode_shared_plan(64, 40, 8, 128, 16, 560, 512, kv_dtype="fp4")
 
 
-def test_packed_descriptors_are_the_c_structs():
-    # what _Call packs for a tensor of each rank is pad_tensor, byte for byte where used
-    for shape in ((3,), (3, 5), (2, 3, 4), (2, 3, 4, 5)):
-        t = torch.zeros(shape, dtype=torch.bfloat16)
-        if len(shape) > 1:
-            t = t.transpose(0, 1)
-        want = pad.describe(t)
-        buf = bytearray(80)
-        n = t.dim()
-        pad._PACK[n].pack_into(buf, 0, t.data_ptr(), pad._DTYPES[t.dtype], n, *t.shape, *t.stride())
-        got = pad.PadTensor.from_buffer(buf)
-        assert (got.data, got.dtype, got.ndim) == (want.data, want.dtype, want.ndim)
-        assert list(got.shape)[:n] == list(want.shape)[:n] and list(got.stride)[:n] == list(want.stride)[:n]
-    assert pad._PACK_APPEND.size == ctypes.sizeof(AppendOptions) and pad._PACK_DECODE.size == ctypes.sizeof(pad.PadOptions)
-    buf = bytearray(64)
-    pad._PACK_APPEND.pack_into(buf, 0, 1, 2, 3, 4.0, 5, 6, 7, 8.0, 9.0)
-    o = AppendOptions.from_buffer(buf)
-    assert (o.inv_freq, o.interleaved, o.k_weight, o.eps, o.q, o.q_weight, o.q_out, o.k_scale, o.v_scale) == \
-        (1, 2, 3, 4.0, 5, 6, 7, 8.0, 9.0)
-    buf = bytearray(24)
-    pad._PACK_DECODE.pack_into(buf, 0, 1, 0, 3.0, 4.0)
-    o = pad.PadOptions.from_buffer(buf)
-    assert (o.window_left, bool(o.sinks), o.k_scale, o.v_scale) == (1, False, 3.0, 4.0)
+def test_the_binding_refuses_what_it_cannot_describe():
+    fast = pad._load_fast()
+    for f, n in ((fast.qk_norm_rope, 11), (fast.append_kv, 17), (fast.decode_shared, 14)):
+        with pytest.raises(TypeError):
+            f()
+        with pytest.raises(TypeError):
+            f(*[None] * n)            # the first tensor is not optional
+        with pytest.raises(ValueError):
+            f(torch.zeros(1, 4, 128, dtype=torch.bfloat16), *[None] * (n - 1))  # not a CUDA tensor
 
 
 def test_the_binding_has_no_cpu_path():
