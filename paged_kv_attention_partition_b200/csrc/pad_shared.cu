@@ -90,37 +90,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-
-// 2^x of two values on the FMA pipe: x = n + f with n the nearest integer (the low
-// bits of x + 1.5 * 2^23), 2^f by the degree-5 polynomial that interpolates it at
-// the Chebyshev nodes of [-1/2, 1/2] (2.5e-7 off at most), 2^n by its exponent
-// field.  Below -126.5 it is 0; NaN stays NaN.
-__device__ __forceinline__ float2 exp2_fma(uint64_t x) {
-  const float2 xc = parts(x);
-  const uint64_t c = duo(max_nan(xc.x, -127.f), max_nan(xc.y, -127.f));
-  const uint64_t t = add2(c, duo(12582912.f, 12582912.f));
-  const uint64_t f = add2(c, mul2(add2(t, duo(-12582912.f, -12582912.f)), duo(-1.f, -1.f)));
-  uint64_t p = duo(0.0013390863f, 0.0013390863f);
-  p = fma2(p, f, duo(0.009676032f, 0.009676032f));
-  p = fma2(p, f, duo(0.05550357f, 0.05550357f));
-  p = fma2(p, f, duo(0.24022107f, 0.24022107f));
-  p = fma2(p, f, duo(0.6931472f, 0.6931472f));
-  p = fma2(p, f, duo(1.0000001f, 1.0000001f));
-  const float2 ti = parts(t);
-  return parts(mul2(p, duo(__uint_as_float((__float_as_uint(ti.x) << 23) + 0x3f800000u),
-                           __uint_as_float((__float_as_uint(ti.y) << 23) + 0x3f800000u))));
-}
-
 // ---- the partial kernel -------------------------------------------------------
 //
 // One persistent CTA per SM, warp-specialised; every role goes through the CTA's
@@ -131,8 +100,8 @@ __device__ __forceinline__ float2 exp2_fma(uint64_t x) {
 //   V warp          the V chunks into another ring
 //   QK warp         S = Q . K^T  (128 rows x chunk) into one of the S buffers
 //   PV warp         O += P . V, P read from tensor memory
-//   softmax warps   two threads per row, half a chunk's columns each: scores out of
-//                   tensor memory, running maximum and sum, P back over the scores
+//   softmax warps   thread = row: scores out of tensor memory, running maximum and
+//                   sum, P back over the scores
 //
 // A step is (query tile, chunk); step n of the CTA uses S buffer n % NBUF and is the
 // buffer's use n / NBUF, which gives every barrier's phase.  A two-tile unit takes both
@@ -140,13 +109,17 @@ __device__ __forceinline__ float2 exp2_fma(uint64_t x) {
 // even and odd chunks between the accumulators, which leave two partials per row.
 // At D = 256 there is one accumulator (256 of the 512 columns) and one softmax group.
 //
-// The P of a step overlays its S, so QK(n + NBUF) waits for PV(n).  The products are
-// issued by two warps because between two of them a warp spends about as long on its
-// waits and counters as the tensor core on a product: from one warp a step (one
-// tile, 128 tokens, D = 128) took 2290 cycles, of which the products' issue was 1165.
+// The P of a step overlays its S, so QK(n + NBUF) waits for PV(n).  Four buffers of 64
+// tokens keep the next scores ready when a group has written P.  Measured on B200,
+// 256 sequences of 32 / 8 heads of 128 behind 32768 shared tokens: 153 us; two
+// buffers of 128 tokens with two threads per row 161 us (rows of 128 scores do not fit
+// one thread's registers); a quarter of the exponentials on the FMA pipe instead
+// of ex2 154 us, half 163 us.  The products are issued by two warps because between
+// two of them a warp spends about as long on its waits and counters as the tensor
+// core on a product: from one warp the products' issue was half of its time.
 template <int D>
 struct SharedCfg {
-  static constexpr int CT = shared_chunk(D), NBUF = 256 / CT, NACC = shared_accs(D), CB = D / 64;
+  static constexpr int CT = kSharedChunk, NBUF = 4, NACC = shared_accs(D), CB = D / 64;
   static constexpr int QR = shared_rows(D);
   static constexpr uint32_t kSlot = CT * D * 2;         // bytes of a K or V chunk
   // A chunk's rows lie in groups of 8, a group's 128-byte column blocks one after
@@ -156,9 +129,9 @@ struct SharedCfg {
   static constexpr uint32_t kQ = CB * kQBlock;
   // Ring slots: what is left beside q.  V's slots are held longer, from the copy
   // to the value product two steps behind the score product.
-  static constexpr int NK = D == 64 ? 4 : 2, NV = D == 64 ? 4 : 3, NS = NK + NV;
+  static constexpr int NK = 512 / D, NV = D == 64 ? 8 : D == 128 ? 6 : 3, NS = NK + NV;
   static constexpr int kQueue = 4;
-  static constexpr int kGroupWarps = 8;                 // a softmax group: 4 x 32 rows, two halves of the columns
+  static constexpr int kGroupWarps = 4;                 // a softmax group: a tile's rows
   static constexpr int kSoftmaxWarps = kGroupWarps * NACC;
   static constexpr int kKWarp = kSoftmaxWarps, kVWarp = kSoftmaxWarps + 1, kQkWarp = kSoftmaxWarps + 2,
                        kPvWarp = kSoftmaxWarps + 3;
@@ -449,33 +422,12 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
     }
     if (tc::elect()) tc::commit(idle);
   } else {
-    // ---- softmax: a row's columns in two halves, one thread each
-    constexpr int HC = CT / 2;
-    constexpr int kExpFma = 1, kExpOf = 4;  // of each four pairs, one on the FMA pipe: ex2 alone is 16 a cycle
-    const int w = warp / C::kGroupWarps, half = warp >> 2 & 1, wq = warp & 3, row_in_tile = wq * 32 + lane;
+    // ---- softmax: thread = row of the group's tile
+    const int w = warp / C::kGroupWarps, wq = warp & 3, row_in_tile = wq * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
-    const uint32_t ocol = lanes + C::kOCol + w * D + half * (D / 2);
-    // The two warps of the same rows exchange a value per row through a column of
-    // tensor memory each (shared memory is full): own, then a barrier, then other.
-    auto exchange = [&](uint32_t own, uint32_t other, float v) -> float {
-      tc::st1(own, v);
-      tc::wait_st();
-      tc::fence_before();
-      asm volatile("bar.sync %0, 64;\n" ::"r"(1 + w * 4 + wq) : "memory");
-      tc::fence_after();
-      return tc::ld1(other);
-    };
-    // Barrier of the two warps that also ORs a value over them.
-    auto any_of_both = [&](bool v) -> bool {
-      uint32_t r;
-      asm volatile(
-          "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.red.or.pred q, %2, 64, p;\n selp.u32 %0, 1, 0, q;\n}\n"
-          : "=r"(r)
-          : "r"((uint32_t)v), "r"(1 + w * 4 + wq)
-          : "memory");
-      return r != 0;
-    };
+    const uint32_t ocol = lanes + C::kOCol + w * D;
     const float sl2 = fabsf(p.scale_log2);  // a negative scale's sign is in the score product
+    const uint64_t scale = duo(sl2, sl2);
     uint32_t step = 0;               // steps of all units so far
     bool ok = true;
     SharedUnit u;
@@ -486,46 +438,43 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
       const int tile = two ? j0 : 0;
       const int r = tile * kTileRows + row_in_tile;
       const bool live = tile * kTileRows + wq * 32 < u.rows;  // the warp has a row
+      int nv = u.tok1 - u.tok0 - (two ? 0 : j0) * CT;         // tokens of the step's chunk and behind it
       float m = -INFINITY, l = 0.f;
-      for (int j = j0; ok && j < steps; j += NACC) {
-        const uint32_t buf = (step + j) % NBUF;
-        ok = __all_sync(0xffffffffu, wait(s_full + 8 * buf, (step + j) / NBUF & 1));
+      for (int j = j0; ok && j < steps; j += NACC, nv -= (two ? 1 : NACC) * CT) {
+        const uint32_t n = step + j, buf = n % NBUF;
+        ok = __all_sync(0xffffffffu, wait(s_full + 8 * buf, n / NBUF & 1));
         if (!ok) break;
         if (live) {
           tc::fence_after();
           const uint32_t scol = lanes + buf * C::kSCol;
-          float s[HC];
-#pragma unroll
-          for (int i = 0; i < HC; i += 32) tc::ld32(scol + half * HC + i, s + i);
+          float s[CT];
+          tc::ld32(scol, s);
+          tc::ld32(scol + 32, s + 32);
           tc::wait_ld();
-          const int nv = u.tok1 - (u.tok0 + (two ? j >> 1 : j) * CT) - half * HC;  // columns in range
-          if (nv < HC) {
+          if (nv < CT) {
 #pragma unroll
-            for (int i = 0; i < HC; ++i)
+            for (int i = 0; i < CT; ++i)
               if (i >= nv) s[i] = -INFINITY;
           }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < HC; i += 2) mx[i >> 1 & 3] = fmaxf(fmaxf(mx[i >> 1 & 3], s[i]), s[i + 1]);
-          float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+          for (int i = 0; i < CT; i += 2) mx[i >> 1 & 3] = fmaxf(fmaxf(mx[i >> 1 & 3], s[i]), s[i + 1]);
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
           // The reference moves only when a score passes it by 2^8: any
           // reference gives the same result as long as l and O share it, and the
-          // exchange of the halves' maxima and the rescale of O are skipped on
-          // almost every chunk.  Behind this barrier both halves of S have been
-          // read: P, in its first half, may overwrite it.
-          if (any_of_both(top > m + 8.f)) {
-            top = fmaxf(top, exchange(scol + half * HC + HC - 1, scol + (half ^ 1) * HC + HC - 1, top));
+          // rescale of O is skipped on almost every chunk.
+          if (__any_sync(0xffffffffu, top > m + 8.f)) {
             const float mn = fmaxf(m, top);
             const float a = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
             m = mn;
             l *= a;
             if (j != j0) {  // O holds the earlier chunks once their product is done
-              const uint32_t n = step + j - NACC;  // the group's step before this one
-              ok = __all_sync(0xffffffffu, wait(pv_done + 8 * (n % NBUF), n / NBUF & 1));
+              const uint32_t before = n - NACC;
+              ok = __all_sync(0xffffffffu, wait(pv_done + 8 * (before % NBUF), before / NBUF & 1));
               if (!ok) break;
               tc::fence_after();
 #pragma unroll 1
-              for (int i = 0; i < D / 2; i += 16) {
+              for (int i = 0; i < D; i += 16) {
                 float o[16];
                 tc::ld16(ocol + i, o);
                 tc::wait_ld();
@@ -536,30 +485,23 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
             }
           }
           const float ref = m == -INFINITY ? 0.f : m;
-          const uint64_t scale = duo(sl2, sl2), shift = duo(-ref, -ref);
+          const uint64_t shift = duo(-ref, -ref);
           uint64_t ls[2] = {0, 0};
 #pragma unroll
-          for (int i = 0; i < HC; i += 32) {
+          for (int i = 0; i < CT; i += 32) {
             uint32_t pk[16];
 #pragma unroll
             for (int x = 0; x < 32; x += 2) {
-              const uint64_t v = fma2(duo(s[i + x], s[i + x + 1]), scale, shift);
-              float2 e;
-              if (x / 2 % kExpOf < kExpFma) {
-                e = exp2_fma(v);
-              } else {
-                e = parts(v);
-                e.x = fast_exp2(e.x);
-                e.y = fast_exp2(e.y);
-              }
+              float2 e = parts(fma2(duo(s[i + x], s[i + x + 1]), scale, shift));
+              e.x = fast_exp2(e.x);
+              e.y = fast_exp2(e.y);
               ls[x >> 1 & 1] = add2(ls[x >> 1 & 1], duo(e.x, e.y));
               pk[x / 2] = pack_bf16x2(e.x, e.y);
             }
-            tc::st16(scol + (half * HC + i) / 2, pk);
+            tc::st16(scol + i / 2, pk);
           }
-          const float2 l2 = parts(add2(ls[0], ls[1]));
-          l += l2.x + l2.y;  // fp32 weights: rounded ones would move lse by up to 2^-9
-          if (j + NACC >= steps) l += exchange(scol + HC + half, scol + HC + (half ^ 1), l);  // the unit's sum
+          const float2 sum = parts(add2(ls[0], ls[1]));
+          l += sum.x + sum.y;  // fp32 weights: rounded ones would move lse by up to 2^-9
           tc::wait_st();
           tc::fence_before();
         }
@@ -573,9 +515,9 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
           tc::fence_after();
           const float inv = 1.f / l;
           const int64_t row = u.part + (two || NACC == 1 ? 0 : (int64_t)j0 * u.rows) + r;
-          float4 *dst = reinterpret_cast<float4 *>(p.o_part + row * D + half * (D / 2));
+          float4 *dst = reinterpret_cast<float4 *>(p.o_part + row * D);
 #pragma unroll
-          for (int i = 0; i < D / 2; i += 32) {
+          for (int i = 0; i < D; i += 32) {
             float o[32];
             tc::ld32(ocol + i, o);
             tc::wait_ld();
@@ -585,7 +527,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
                 dst[i / 4 + x] = make_float4(o[4 * x] * inv, o[4 * x + 1] * inv, o[4 * x + 2] * inv, o[4 * x + 3] * inv);
             }
           }
-          if (half == 0 && r < u.rows) p.lse_part[row] = m + log2f(l);
+          if (r < u.rows) p.lse_part[row] = m + log2f(l);
           tc::fence_before();
         }
         __syncwarp();
@@ -651,7 +593,7 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const __grid_constant
   if (L > Lp) {
     const int64_t cost = shared_rest_cost<D>(p, L);
     const int k = kvh * p.HT + ht;
-    ri = make(p.cum[b] + k * cost, cost, p.w_rest, (L - Lp + shared_chunk(D) - 1) / shared_chunk(D),
+    ri = make(p.cum[b] + k * cost, cost, p.w_rest, (L - Lp + kSharedChunk - 1) / kSharedChunk,
               p.rest_row0 + ((int64_t)b * p.Hkv * p.HT + k) * p.rest_rows, p.rest_rows, p.gt, j);
   }
   float m = -INFINITY, l = 0.f, acc[VEC];

@@ -29,7 +29,7 @@ constexpr int kTileRows = 128;  // query rows of one tensor-core tile
 // half of the tensor memory).
 __host__ __device__ constexpr int shared_rows(int D) { return D == 256 ? kTileRows : 2 * kTileRows; }
 // Tokens of a chunk.
-__host__ __device__ constexpr int shared_chunk(int D) { return D == 256 ? 64 : 128; }
+constexpr int kSharedChunk = 64;
 // Accumulators: two tiles of rows, or one tile's even and odd chunks.
 __host__ __device__ constexpr int shared_accs(int D) { return D == 256 ? 1 : 2; }
 

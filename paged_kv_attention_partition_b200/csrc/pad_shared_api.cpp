@@ -170,7 +170,7 @@ extern "C" pad_status pad_decode_shared_plan(int64_t batch, int64_t num_q_heads,
   pad::SharedParams p{};
   const Layout l = layout(s, pad::host_sm_count(device < 0 ? 0 : device), &p);
   plan->ctas = p.ctas;
-  plan->chunk_tokens = pad::shared_chunk((int)head_dim);
+  plan->chunk_tokens = pad::kSharedChunk;
   plan->prefix_rows = p.nseq * p.gt;
   plan->prefix_blocks = p.nrb * p.HT;
   plan->workspace_bytes = batch == 0 ? 0 : (int64_t)l.total;
@@ -274,7 +274,7 @@ extern "C" pad_status pad_decode_shared(const pad_tensor *q, const pad_tensor *k
   } else if ((st = pad::host_scratch(device, stream, l.total, &workspace)) != PAD_OK) {
     return st;
   }
-  choose_box(k_cache, v_cache, pad::shared_chunk((int)D), &p);
+  choose_box(k_cache, v_cache, pad::kSharedChunk, &p);
   if (!fp8) {
     if ((st = cache_map(&p.tmk, k_cache, p, "k_cache")) != PAD_OK) return st;
     if ((st = cache_map(&p.tmv, v_cache, p, "v_cache")) != PAD_OK) return st;

@@ -37,7 +37,7 @@ __device__ __forceinline__ int shared_len(const SharedParams &p, int b, bool *ba
 template <int D>
 __device__ __forceinline__ int64_t shared_rest_cost(const SharedParams &p, int L) {
   const int n = L - (p.n_shared << p.bs_log2);
-  return n <= 0 ? 0 : p.w_item + (int64_t)((n + shared_chunk(D) - 1) / shared_chunk(D)) * p.w_rest;
+  return n <= 0 ? 0 : p.w_item + (int64_t)((n + kSharedChunk - 1) / kSharedChunk) * p.w_rest;
 }
 
 // The prefix part of the line: items (kvh, ht, rb), rb innermost; every row block
@@ -49,7 +49,7 @@ struct SharedPrefix {
 template <int D>
 __device__ __forceinline__ SharedPrefix shared_prefix(const SharedParams &p) {
   SharedPrefix s;
-  s.chunks = ((p.n_shared << p.bs_log2) + shared_chunk(D) - 1) / shared_chunk(D);
+  s.chunks = ((p.n_shared << p.bs_log2) + kSharedChunk - 1) / kSharedChunk;
   s.last_nb = p.B - (p.nrb - 1) * p.nseq;
   auto cost = [&](int nb) -> int64_t {
     return s.chunks == 0 ? 0 : p.w_item + (int64_t)s.chunks * (nb * p.gt > kTileRows ? p.w_pre2 : p.w_pre1);
@@ -73,7 +73,7 @@ __device__ __forceinline__ int shared_cut(const SharedParams &p, int64_t at, int
 // cum != null: also writes the rest items' cumulative costs.
 template <int D, class Emit>
 __device__ __forceinline__ void shared_walk(const SharedParams &p, int cta, int64_t *cum, Emit &&emit) {
-  constexpr int CT = shared_chunk(D);
+  constexpr int CT = kSharedChunk;
   const int lane = threadIdx.x & 31;
   const SharedPrefix pre = shared_prefix<D>(p);
   const int Lp = p.n_shared << p.bs_log2;

@@ -180,7 +180,7 @@ def test_shared_empty_batch_is_a_no_op(lib):
 def test_shared_plan(lib):
     p = pad.pad_decode_shared_plan(64, 40, 8, 128, 16, 560, 512, device=0)
     # 51 sequences x 5 heads share a pass (two 128-row tiles), 13 the second one
-    assert (p["ctas"], p["chunk_tokens"], p["prefix_rows"], p["prefix_blocks"]) == (148, 128, 255, 2)
+    assert (p["ctas"], p["chunk_tokens"], p["prefix_rows"], p["prefix_blocks"]) == (148, 64, 255, 2)
     # room for the partials of every (row block, KV head) and (sequence, KV head), each cut at
     # most once per CTA: fp32 rows of D + 1
     rows = (8 * 2 + 148) * 255 + (64 * 8 + 148) * 2 * 5
