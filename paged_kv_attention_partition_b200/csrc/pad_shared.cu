@@ -18,56 +18,6 @@
 namespace pad {
 namespace {
 
-// One warp per query row, one token at a time: the definition, as a kernel.
-template <int D, bool F8>
-__global__ void __launch_bounds__(256) shared_kernel(const __grid_constant__ SharedParams p) {
-  constexpr int VEC = D / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  shared_walk<D>(p, blockIdx.x, blockIdx.x == 0 && warp == 0 ? p.cum : nullptr, [&](const SharedUnit &u) {
-    for (int r = warp; r < u.rows; r += 8) {
-      const int b = u.b0 + r / p.gt, j = r % p.gt;
-      if (j >= u.heads) continue;
-      const int h = u.kvh * p.g + u.ht * p.gt + j;
-      float qv[VEC], acc[VEC], m = -INFINITY, l = 0.f;
-      for (int i = 0; i < VEC; ++i) {
-        qv[i] = __uint_as_float((uint32_t)p.q[b * p.q_sb + (int64_t)h * p.q_sh + lane * VEC + i] << 16) * p.scale_log2;
-        acc[i] = 0.f;
-      }
-      for (int t = u.tok0; t < u.tok1; ++t) {
-        const int pg = t >> p.bs_log2, slot = t & ((1 << p.bs_log2) - 1);
-        const int id = pg < p.n_shared ? p.shared_table[pg] : p.tables[b * p.table_stride + pg];
-        const bool ok = (unsigned)id < (unsigned)p.num_blocks;
-        if (!ok && lane == 0) atomicOr(p.err, kErrBlockId);
-        const int64_t ko = id * p.k_sblk + u.kvh * p.k_sh + slot * p.k_ss + lane * VEC;
-        const int64_t vo = id * p.v_sblk + u.kvh * p.v_sh + slot * p.v_ss + lane * VEC;
-        auto at = [&](const void *c, int64_t o) -> float {
-          if (!ok) return 0.f;
-          if constexpr (F8) {
-            const uint32_t h2 = e4m3x2_to_f16x2(static_cast<const uint8_t *>(c)[o]);
-            return __half2float(__ushort_as_half((unsigned short)h2));
-          } else {
-            return __uint_as_float((uint32_t)static_cast<const uint16_t *>(c)[o] << 16);
-          }
-        };
-        float s = 0.f;
-        for (int i = 0; i < VEC; ++i) s += qv[i] * at(p.k, ko + i);
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.f : mn;
-        const float a = exp2f(m - ref), w = exp2f(s - ref);
-        m = mn;
-        l = l * a + w;
-        for (int i = 0; i < VEC; ++i) acc[i] = acc[i] * a + w * at(p.v, vo + i);
-      }
-      const int64_t row = u.part + r;
-      for (int i = 0; i < VEC; ++i) p.o_part[row * D + lane * VEC + i] = acc[i] / l;
-      if (lane == 0) {
-        p.lse_part[row] = m + log2f(l);
-        if (shared_part_rows(u.rows, D) != u.rows) p.lse_part[row + u.rows] = -INFINITY;
-      }
-    }
-  });
-}
-
 // ---- arithmetic of the softmax, two values at a time ----------------------------
 
 __device__ __forceinline__ uint64_t duo(float lo, float hi) {
@@ -102,6 +52,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 //   PV warp         O += P . V, P read from tensor memory
 //   softmax warps   thread = row: scores out of tensor memory, running maximum and
 //                   sum, P back over the scores
+//   widening warps  (E4M3 cache) the copies' codes, from a small ring of their own, to
+//                   f16 operands: two warps for q and K, two for V
+//
+// Every E4M3 code is an f16 value, and q is scaled per row by a power of two that
+// puts its largest element into [2^14, 2^15), where its bf16 values are f16 values
+// too (down to 2^-28 of that element); the row's score scale takes the inverse.  P is
+// f16 then, three bits finer than bf16.
 //
 // A step is (query tile, chunk); step n of the CTA uses S buffer n % NBUF and is the
 // buffer's use n / NBUF, which gives every barrier's phase.  A two-tile unit takes both
@@ -117,7 +74,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // of ex2 154 us, half 163 us.  The products are issued by two warps because between
 // two of them a warp spends about as long on its waits and counters as the tensor
 // core on a product: from one warp the products' issue was half of its time.
-template <int D>
+template <int D, bool F8>
 struct SharedCfg {
   static constexpr int CT = kSharedChunk, NBUF = 4, NACC = shared_accs(D), CB = D / 64;
   static constexpr int QR = shared_rows(D);
@@ -129,22 +86,40 @@ struct SharedCfg {
   static constexpr uint32_t kQ = CB * kQBlock;
   // Ring slots: what is left beside q.  V's slots are held longer, from the copy
   // to the value product two steps behind the score product.
-  static constexpr int NK = 512 / D, NV = D == 64 ? 8 : D == 128 ? 6 : 3, NS = NK + NV;
+  static constexpr int NK = 512 / D, NV = D == 64 ? 8 : F8 ? NK : D == 128 ? 6 : 3, NS = NK + NV;
+  // E4M3: slots of codes, per ring; rows of boxes of at least 128 bytes
+  static constexpr int NR = F8 ? (D == 256 ? 1 : 2) : 0;
+  static constexpr uint32_t kRaw = CT * (D < 128 ? 128 : D);
   static constexpr int kQueue = 4;
   static constexpr int kGroupWarps = 4;                 // a softmax group: a tile's rows
   static constexpr int kSoftmaxWarps = kGroupWarps * NACC;
   static constexpr int kKWarp = kSoftmaxWarps, kVWarp = kSoftmaxWarps + 1, kQkWarp = kSoftmaxWarps + 2,
-                       kPvWarp = kSoftmaxWarps + 3;
-  static constexpr int kThreads = (kSoftmaxWarps + 4) * 32;
-  static constexpr uint32_t ring = kQ, queue = ring + NS * kSlot, bars = queue + kQueue * 64;
-  static constexpr uint32_t total = bars + 512 + 1024 /* alignment slack */;
+                       kPvWarp = kSoftmaxWarps + 3, kWidenWarp = kSoftmaxWarps + 4;
+  static constexpr int kWarps = kSoftmaxWarps + (F8 ? 8 : 4), kThreads = kWarps * 32;
+  static constexpr uint32_t ring = kQ, raw = ring + NS * kSlot, queue = raw + 2 * NR * kRaw,
+                            bars = queue + kQueue * 64;
+  static constexpr uint32_t kBarBytes = 640, total = bars + kBarBytes + 1024 /* alignment slack */;
   static constexpr uint32_t kSCol = CT, kOCol = NBUF * CT;  // tensor memory: S buffers, then O
 };
 static_assert(sizeof(SharedUnit) <= 64, "queue entry");
 
-template <int D>
-__global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(const __grid_constant__ SharedParams p) {
-  using C = SharedCfg<D>;
+// Power of two that scales a row of bf16 q whose largest magnitude has these bits
+// into f16's range, as an exponent; 0 for a row of zeros or one that is not finite.
+__device__ __forceinline__ int q_exponent(uint32_t abs_bits) {
+  return abs_bits == 0 || abs_bits >= 0x7f80u ? 0 : min(100, max(-100, 141 - (int)(abs_bits >> 7)));
+}
+__device__ __forceinline__ uint32_t max_abs(uint32_t m, const uint4 &c) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7fffu, w[i] >> 16 & 0x7fffu));
+  return m;
+}
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }
+
+template <int D, bool F8>
+__global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
+    shared_kernel(const __grid_constant__ SharedParams p) {
+  using C = SharedCfg<D, F8>;
   constexpr int CT = C::CT, NACC = C::NACC, NBUF = C::NBUF, NS = C::NS, CB = C::CB;
   static_assert(C::total <= (uint32_t)kSmemBudget, "shared-memory plan over budget");
   static_assert(C::kOCol + NACC * D <= 512, "tensor memory");
@@ -157,20 +132,22 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
   const uint32_t full = bar0, empty = full + 8 * NS, q_full = empty + 8 * NS, q_empty = q_full + 16,
                  s_full = q_empty + 16, p_full = s_full + 8 * NBUF, pv_done = p_full + 8 * NBUF,
                  o_free = pv_done + 8 * NBUF,
-                 u_full = o_free + 16, u_empty = u_full + 8 * C::kQueue, idle = u_empty + 8 * C::kQueue;
-  constexpr int kBars = 2 * NS + 3 * NBUF + 6 + 2 * C::kQueue + 1;
-  static_assert(kBars * 8 + 8 <= 512, "barrier area");
+                 u_full = o_free + 16, u_empty = u_full + 8 * C::kQueue, idle = u_empty + 8 * C::kQueue,
+                 q_tx = F8 ? idle + 8 : q_full, raw_full = q_tx + 16, raw_empty = raw_full + 16 * C::NR;
+  constexpr int kBars = 2 * NS + 3 * NBUF + 6 + 2 * C::kQueue + 1 + (F8 ? 2 + 4 * C::NR : 0);
+  static_assert(kBars * 8 + 8 <= C::kBarBytes, "barrier area");
   uint32_t *words = reinterpret_cast<uint32_t *>(bars + kBars);  // [0] tmem, [1] abort
   volatile int *abort_flag = reinterpret_cast<volatile int *>(words + 1);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(full + 8 * i, 1);
+      mbar_init(full + 8 * i, F8 ? 2 : 1);  // a ring's widening warps, or the copy
       mbar_init(empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + 8 * i, 1);
+      mbar_init(q_full + 8 * i, F8 ? 2 : 1);
+      if (F8) mbar_init(q_tx + 8 * i, 1);
       mbar_init(q_empty + 8 * i, 1);
       mbar_init(o_free + 8 * i, C::kGroupWarps);
     }
@@ -181,7 +158,11 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
     }
     for (int i = 0; i < C::kQueue; ++i) {
       mbar_init(u_full + 8 * i, 1);
-      mbar_init(u_empty + 8 * i, C::kSoftmaxWarps + 3);  // every role's warps
+      mbar_init(u_empty + 8 * i, C::kWarps - 1);  // every warp but the one that fills it
+    }
+    for (int i = 0; i < 2 * C::NR; ++i) {
+      mbar_init(raw_full + 8 * i, 1);
+      mbar_init(raw_empty + 8 * i, 2);
     }
     mbar_init(idle, 2);
     *abort_flag = 0;
@@ -213,7 +194,8 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
   // rows, else each half in turn (one at D = 256).
   auto q_box_rows = [&](const SharedUnit &u) { return p.gt * (u.rest ? 1 : p.nseq); };
 
-  // One ring's chunks of a unit, by a whole warp: K's or V's.
+  // One ring's chunks of a unit, by a whole warp: K's or V's.  (E4M3: its codes' ring.)
+  const uint32_t copied = F8 ? raw_full : full, freed = F8 ? raw_empty : empty;
   uint32_t slot = 0, phase = 1, used = 0;  // a first filling's wait passes at once
   auto copy_chunks = [&](const SharedUnit &u, const CUtensorMap *map, uint32_t first_slot, uint32_t slots) -> bool {
     const int32_t *table = u.rest ? p.tables + u.b0 * p.table_stride : p.shared_table;
@@ -232,10 +214,11 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
     for (int c = 0; c < u.chunks; ++c) {
       int id = id_next;
       id_next = fetch(c + 1, 0);  // a chunk ahead: the table's latency is not in the copies' way
-      const uint32_t bar = full + 8 * (first_slot + slot), dst = sring + (first_slot + slot) * C::kSlot;
-      if (!__all_sync(0xffffffffu, wait(empty + 8 * (first_slot + slot), phase))) return false;
+      const uint32_t bar = copied + 8 * (first_slot + slot);
+      const uint32_t dst = F8 ? sq + C::raw + (first_slot + slot) * C::kRaw : sring + (first_slot + slot) * C::kSlot;
+      if (!__all_sync(0xffffffffu, wait(freed + 8 * (first_slot + slot), phase))) return false;
       const bool one = tc::elect();
-      if (one) mbar_arrive_expect_tx(bar, C::kSlot);
+      if (one) mbar_arrive_expect_tx(bar, F8 ? CT * D : C::kSlot);
       // a box's first row inside its page: only pages larger than a box have several
       const int in_page = (u.tok0 + c * CT) & ((1 << p.bs_log2) - 1);
 #pragma unroll 1
@@ -245,9 +228,11 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
         for (int jj = 0; jj < 32 && 32 * w + jj < nbox; ++jj) {
           const int j = 32 * w + jj, blk = __shfl_sync(0xffffffffu, id, jj), row = j << box_log2;
           const int at = box_log2 < p.bs_log2 ? (in_page + row) & ((1 << p.bs_log2) - 1) : 0;
-          const uint32_t to = dst + (row >> 3) * C::kGroup + (row & 7) * 128;
+          const uint32_t to = F8 ? dst + j * p.box_pitch : dst + (row >> 3) * C::kGroup + (row & 7) * 128;
           if (one) {
-            if (p.box_kind == kBoxPage) {  // a page, or a chunk's worth of a larger one
+            if constexpr (F8) {
+              tma_load_4d(to, map, 0, at, u.kvh, blk, bar);
+            } else if (p.box_kind == kBoxPage) {  // a page, or a chunk's worth of a larger one
               tma_load_5d(to, map, 0, 0, 0, at >> 3, blk * p.blk_heads + u.kvh, bar);
             } else if (p.box_kind == kBoxGroup) {  // 8 rows
               tma_load_5d(to, map, 0, at, 0, u.kvh, blk, bar);
@@ -272,7 +257,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
   auto drain = [&](uint32_t first_slot, uint32_t slots) {
     if (lane == 0)
       for (uint32_t i = used > slots ? used - slots : 0; i < used; ++i)
-        wait(full + 8 * (first_slot + i % slots), (i / slots) & 1, true);
+        wait(copied + 8 * (first_slot + i % slots), (i / slots) & 1, true);
   };
 
   if (warp == C::kKWarp) {
@@ -298,29 +283,30 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
       if (both) ok = ok && __all_sync(0xffffffffu, wait(q_empty + 8, qphase >> 1));
       if (!ok) return;
       if (tc::elect()) {
-        mbar_arrive_expect_tx(q_full + 8 * h, (uint32_t)box_rows * 128 * CB);
-        if (both) tc::arrive(q_full + 8);
+        mbar_arrive_expect_tx(q_tx + 8 * h, (uint32_t)box_rows * 128 * CB);
+        if (both) tc::arrive(q_tx + 8);
         for (int cb = 0; cb < CB; ++cb)
           tma_load_4d(sq + cb * C::kQBlock + h * (kTileRows * 128), u.rest ? &p.tmqr : &p.tmqp, 0,
-                      u.kvh * p.g + u.ht * p.gt, cb, u.b0, q_full + 8 * h);
+                      u.kvh * p.g + u.ht * p.gt, cb, u.b0, q_tx + 8 * h);
       }
       __syncwarp();
       qphase ^= both ? 3 : 1 << h;
       q_used[h] = true;
-      ok = copy_chunks(u, &p.tmk, 0, C::NK);
+      ok = copy_chunks(u, &p.tmk, 0, F8 ? C::NR : C::NK);
     });
     put(SharedUnit{});  // chunks == 0: the end
-    drain(0, C::NK);
+    drain(0, F8 ? C::NR : C::NK);
     if (lane == 0)
       for (int h = 0; h < 2; ++h)
-        if (q_used[h]) wait(q_full + 8 * h, qphase >> h & 1, true);
+        if (q_used[h]) wait(q_tx + 8 * h, qphase >> h & 1, true);
   } else if (warp == C::kVWarp) {
     bool ok = true;
     SharedUnit u;
-    for (int k = 0; ok && (ok = next_unit(k, u)) && u.chunks > 0; ++k) ok = copy_chunks(u, &p.tmv, C::NK, C::NV);
-    drain(C::NK, C::NV);
+    constexpr uint32_t first = F8 ? C::NR : C::NK, slots = F8 ? C::NR : C::NV;
+    for (int k = 0; ok && (ok = next_unit(k, u)) && u.chunks > 0; ++k) ok = copy_chunks(u, &p.tmv, first, slots);
+    drain(first, slots);
   } else if (warp == C::kQkWarp) {
-    const uint32_t idesc = tc::idesc(CT, false, false) | (p.scale_log2 < 0.f ? tc::kNegateA : 0u);
+    const uint32_t idesc = tc::idesc(CT, false, F8) | (p.scale_log2 < 0.f ? tc::kNegateA : 0u);
     const uint64_t qd0 = tc::smem_desc(sq, 16, 1024), kd0 = tc::smem_desc(sring, 16, C::kGroup);
     uint32_t kslot = 0, kphase = 0, n = 0;  // ring slot and its phase, steps so far
     uint32_t qphase = 0;                    // a bit per half of q
@@ -368,7 +354,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
     }
     if (tc::elect()) tc::commit(idle);  // every product issued above has completed when this arrives
   } else if (warp == C::kPvWarp) {
-    constexpr uint32_t idesc = tc::idesc(D, true, false);
+    constexpr uint32_t idesc = tc::idesc(D, true, F8);
     const uint64_t vd0 = tc::smem_desc(sring + C::NK * C::kSlot, 1024, C::kGroup);
     uint32_t vslot = 0, vphase = 0, n = 0;
     uint32_t ophase = 3;  // a bit per accumulator; the first wait on each passes at once
@@ -400,7 +386,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
       for (int c = 0; ok && c < u.chunks; ++c) {
         ok = all(wait(full + 8 * (C::NK + vslot), vphase));
         const int nv = u.tok1 - (u.tok0 + c * CT), bs = 1 << p.bs_log2;
-        if (ok && nv < CT && (u.tok1 & (bs - 1)) != 0) {
+        if (!F8 && ok && nv < CT && (u.tok1 & (bs - 1)) != 0) {
           // The page the sequence ends in arrived whole: zeros over the slots behind
           // the sequence, whatever they hold (a weight of 0 times NaN is NaN).
           const int end = min(CT, nv + bs - (u.tok1 & (bs - 1)));
@@ -421,13 +407,95 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
       }
     }
     if (tc::elect()) tc::commit(idle);
+  } else if (F8 && warp >= C::kWidenWarp) {
+    const bool is_k = warp < C::kWidenWarp + 2;
+    const int t = (warp & 1) * 32 + lane;  // (kWidenWarp is even) of the ring's 64 threads
+    constexpr int LR = D / 16;             // threads of a row: 16 codes each
+    const uint32_t first = is_k ? 0 : C::NK, slots = is_k ? C::NK : C::NV, raw0 = is_k ? 0 : C::NR;
+    uint32_t slot = 0, phase = 1, rslot = 0, rphase = 0, qphase = 0;
+    int half = 0;
+    bool ok = true;
+    auto all = [&](bool v) { return __all_sync(0xffffffffu, v) != 0; };
+    SharedUnit u;
+    for (int k = 0; ok && (ok = next_unit(k, u)) && u.chunks > 0; ++k) {
+      if (is_k) {  // ---- q: bf16 to f16 in place, a thread per row
+        const bool both = NACC == 2 && q_box_rows(u) > kTileRows;
+        const int h = both || NACC == 1 ? 0 : half;
+        if (!both && NACC == 2) half ^= 1;
+        ok = all(wait(q_tx + 8 * h, qphase >> h & 1)) && (!both || all(wait(q_tx + 8, qphase >> 1)));
+        if (!ok) break;
+        qphase ^= both ? 3 : 1 << h;
+        for (int r = t; r < u.rows; r += 64) {
+          uint8_t *row = smem + (h * kTileRows + r) * 128;
+          uint32_t m = 0;
+#pragma unroll
+          for (int c = 0; c < CB * 8; ++c)
+            m = max_abs(m, *reinterpret_cast<const uint4 *>(row + (c >> 3) * C::kQBlock + ((c ^ r) & 7) * 16));
+          const float f = pow2(q_exponent(m));
+#pragma unroll
+          for (int c = 0; c < CB * 8; ++c) {
+            uint32_t *x = reinterpret_cast<uint32_t *>(row + (c >> 3) * C::kQBlock + ((c ^ r) & 7) * 16);
+            uint4 v = *reinterpret_cast<const uint4 *>(x);
+            v.x = pack_f16x2(__uint_as_float(v.x << 16) * f, __uint_as_float(v.x & 0xffff0000u) * f);
+            v.y = pack_f16x2(__uint_as_float(v.y << 16) * f, __uint_as_float(v.y & 0xffff0000u) * f);
+            v.z = pack_f16x2(__uint_as_float(v.z << 16) * f, __uint_as_float(v.z & 0xffff0000u) * f);
+            v.w = pack_f16x2(__uint_as_float(v.w << 16) * f, __uint_as_float(v.w & 0xffff0000u) * f);
+            *reinterpret_cast<uint4 *>(x) = v;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tc::arrive(q_full + 8 * h);
+          if (both) tc::arrive(q_full + 8);
+        }
+      }
+      for (int c = 0; c < u.chunks; ++c) {
+        const uint32_t r = raw0 + rslot, s = first + slot;
+        ok = all(wait(raw_full + 8 * r, rphase)) && all(wait(empty + 8 * s, phase));
+        if (!ok) break;
+        const uint8_t *raw = smem + C::raw + r * C::kRaw;
+        uint8_t *to = smem + C::ring + s * C::kSlot;
+        const int nv = is_k ? CT : u.tok1 - (u.tok0 + c * CT);  // V: zeros behind the unit's tokens
+        const int in_box = (1 << p.box_log2) - 1;
+#pragma unroll
+        for (int i = 0; i < LR; ++i) {
+          const int row = i * (64 / LR) + t / LR, x = t % LR;
+          const uint4 v = row < nv ? *reinterpret_cast<const uint4 *>(raw + (row >> p.box_log2) * p.box_pitch +
+                                                                      (row & in_box) * D + x * 16)
+                                   : make_uint4(0, 0, 0, 0);
+          uint4 a, b;  // codes 0-7 and 8-15
+          e4m3x4_to_f16x2x2(v.x, a.x, a.y);
+          e4m3x4_to_f16x2x2(v.y, a.z, a.w);
+          e4m3x4_to_f16x2x2(v.z, b.x, b.y);
+          e4m3x4_to_f16x2x2(v.w, b.z, b.w);
+          uint8_t *d = to + (row >> 3) * C::kGroup + (x >> 2) * 1024 + (row & 7) * 128;
+          const int c0 = (2 * (x & 3)) ^ (row & 7), odd = x >> 2 & 1;  // odd blocks store their second chunk first:
+          *reinterpret_cast<uint4 *>(d + (c0 ^ odd) * 16) = odd ? b : a;  // eight threads, eight 16-byte banks
+          *reinterpret_cast<uint4 *>(d + (c0 ^ odd ^ 1) * 16) = odd ? a : b;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tc::arrive(full + 8 * s);
+          tc::arrive(raw_empty + 8 * r);
+        }
+        if (++slot == slots) {
+          slot = 0;
+          phase ^= 1;
+        }
+        if (++rslot == (uint32_t)C::NR) {
+          rslot = 0;
+          rphase ^= 1;
+        }
+      }
+    }
   } else {
     // ---- softmax: thread = row of the group's tile
     const int w = warp / C::kGroupWarps, wq = warp & 3, row_in_tile = wq * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(wq * 32) << 16);
     const uint32_t ocol = lanes + C::kOCol + w * D;
-    const float sl2 = fabsf(p.scale_log2);  // a negative scale's sign is in the score product
-    const uint64_t scale = duo(sl2, sl2);
+    float sl2 = fabsf(p.scale_log2);  // a negative scale's sign is in the score product
     uint32_t step = 0;               // steps of all units so far
     bool ok = true;
     SharedUnit u;
@@ -440,6 +508,17 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
       const bool live = tile * kTileRows + wq * 32 < u.rows;  // the warp has a row
       int nv = u.tok1 - u.tok0 - (two ? 0 : j0) * CT;         // tokens of the step's chunk and behind it
       float m = -INFINITY, l = 0.f;
+      if constexpr (F8) {  // the power of two that the row's q was scaled by
+        const int bi = r / p.gt, head = r - bi * p.gt;
+        uint32_t top = 0;
+        if (r < u.rows && head < u.heads) {
+          const uint16_t *q = p.q + (u.b0 + bi) * p.q_sb + (int64_t)(u.kvh * p.g + u.ht * p.gt + head) * p.q_sh;
+#pragma unroll
+          for (int i = 0; i < D; i += 8) top = max_abs(top, __ldg(reinterpret_cast<const uint4 *>(q + i)));
+        }
+        sl2 = fabsf(p.scale_log2) * pow2(-q_exponent(top));
+      }
+      const uint64_t scale = duo(sl2, sl2);
       for (int j = j0; ok && j < steps; j += NACC, nv -= (two ? 1 : NACC) * CT) {
         const uint32_t n = step + j, buf = n % NBUF;
         ok = __all_sync(0xffffffffu, wait(s_full + 8 * buf, n / NBUF & 1));
@@ -496,7 +575,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::kThreads, 1) shared_tc_kernel(co
               e.x = fast_exp2(e.x);
               e.y = fast_exp2(e.y);
               ls[x >> 1 & 1] = add2(ls[x >> 1 & 1], duo(e.x, e.y));
-              pk[x / 2] = pack_bf16x2(e.x, e.y);
+              pk[x / 2] = F8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
             }
             tc::st16(scol + i / 2, pk);
           }
@@ -672,22 +751,18 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const __grid_constant
 
 template <int D, bool F8>
 cudaError_t launch_t(const SharedParams &p, cudaStream_t s) {
-  cudaError_t e;
-  if constexpr (F8) {
-    shared_kernel<D, F8><<<p.ctas, 256, 0, s>>>(p);
-  } else {
-    static std::atomic<uint64_t> attr_done{0};
-    int dev = 0;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
-    const uint64_t bit = 1ull << (dev & 63);
-    if (!(attr_done.load(std::memory_order_acquire) & bit)) {
-      e = cudaFuncSetAttribute(shared_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)SharedCfg<D>::total);
-      if (e != cudaSuccess) return e;
-      attr_done.fetch_or(bit, std::memory_order_acq_rel);
-    }
-    shared_tc_kernel<D><<<p.ctas, SharedCfg<D>::kThreads, SharedCfg<D>::total, s>>>(p);
+  using C = SharedCfg<D, F8>;
+  static std::atomic<uint64_t> attr_done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (!(attr_done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(shared_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::total);
+    if (e != cudaSuccess) return e;
+    attr_done.fetch_or(bit, std::memory_order_acq_rel);
   }
+  shared_kernel<D, F8><<<p.ctas, C::kThreads, C::total, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int64_t rows = (int64_t)p.B * p.Hq;
   // comes up while the partial kernel's last CTAs run; waits for them before its first read

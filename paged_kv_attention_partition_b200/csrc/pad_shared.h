@@ -39,6 +39,7 @@ enum SharedBox : int32_t {
   kBoxPage = 0,   // a page's rows (at most a chunk's): (128 bytes, 8 rows, column blocks, row groups, block and head)
   kBoxGroup = 1,  // 8 rows: (128 bytes, 8 rows, column blocks, head, block), for caches whose block stride is not
                   // a multiple of the head stride
+  // (an E4M3 cache: a page's rows, at most a chunk's, as they are: (head_dim, slot, head, block))
   kBoxRows = 2,   // pages below 8 slots: one column block of a page: (128 bytes, rows, column block, head, block)
 };
 
@@ -47,8 +48,6 @@ struct SharedParams {
   CUtensorMap tmqp, tmqr;  // q: boxes of 64 head_dim x gt heads x nseq sequences (prefix), x 1 (rest)
   const uint16_t *q;
   int64_t q_sb, q_sh;
-  const void *k, *v;
-  int64_t k_sblk, k_sh, k_ss, v_sblk, v_sh, v_ss;
   const int32_t *shared_table;
   const int32_t *tables;
   int64_t table_stride;
@@ -61,6 +60,7 @@ struct SharedParams {
   int32_t nseq, nrb;   // sequences of a prefix row block, row blocks
   int32_t bs_log2;
   int32_t box_kind, box_log2;  // SharedBox, rows of a box
+  int32_t box_pitch;           // E4M3: bytes from box to box, at least 128
   int32_t blk_heads;           // kBoxPage: block stride / head stride
   int32_t ctas;
   int32_t w_item, w_pre1, w_pre2, w_rest;  // cost of an item; of a prefix chunk of one and two tiles, of a rest chunk

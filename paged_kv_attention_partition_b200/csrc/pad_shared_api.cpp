@@ -75,6 +75,13 @@ Layout layout(const Shape &s, int ctas, pad::SharedParams *p) {
 void choose_box(const pad_tensor *k, const pad_tensor *v, int chunk, pad::SharedParams *p) {
   const int64_t NB = k->shape[0], H = k->shape[1], bs = k->shape[2];
   p->blk_heads = 1;
+  if (k->dtype == PAD_FP8_E4M3) {
+    p->box_log2 = 0;
+    while ((1 << p->box_log2) < chunk && (1 << p->box_log2) < bs) ++p->box_log2;
+    p->box_pitch = (int32_t)(k->shape[3] << p->box_log2);
+    if (p->box_pitch < 128) p->box_pitch = 128;
+    return;
+  }
   if (bs < 8) {
     p->box_kind = pad::kBoxRows;
     p->box_log2 = p->bs_log2;
@@ -95,16 +102,25 @@ void choose_box(const pad_tensor *k, const pad_tensor *v, int chunk, pad::Shared
   while ((1 << p->box_log2) < chunk && (1 << p->box_log2) < bs) ++p->box_log2;
 }
 
-// A bf16 cache's tensor map for the boxes of `p`, 128-byte swizzle.
+// A cache's tensor map for the boxes of `p`: bf16 with the 128-byte swizzle, E4M3
+// codes as they are (they are widened on the way to the operand).
 pad_status cache_map(CUtensorMap *map, const pad_tensor *t, const pad::SharedParams &p, const char *name) {
   pad::TensorMapEncodeFn enc = pad::host_tensor_map_encoder();
   if (enc == nullptr) return host_fail(PAD_ERR_CUDA, "the CUDA driver does not provide cuTensorMapEncodeTiled");
   const cuuint64_t NB = t->shape[0], H = t->shape[1], bs = t->shape[2], CB = t->shape[3] / 64;
-  auto bytes = [&](int i, int64_t natural) { return (cuuint64_t)(t->shape[i] > 1 ? t->stride[i] * 2 : natural); };
-  const cuuint64_t row = bytes(2, t->shape[3] * 2), head = bytes(1, bs * row), block = bytes(0, H * head);
+  const bool fp8 = t->dtype == PAD_FP8_E4M3;
+  const int64_t eb = fp8 ? 1 : 2;
+  auto bytes = [&](int i, int64_t natural) { return (cuuint64_t)(t->shape[i] > 1 ? t->stride[i] * eb : natural); };
+  const cuuint64_t row = bytes(2, t->shape[3] * eb), head = bytes(1, bs * row), block = bytes(0, H * head);
   const cuuint32_t one[5] = {1, 1, 1, 1, 1};
   CUresult r;
-  if (p.box_kind == pad::kBoxPage) {
+  if (fp8) {
+    const cuuint64_t dims[4] = {(cuuint64_t)t->shape[3], bs, H, NB};
+    const cuuint64_t strides[3] = {row, head, block};
+    const cuuint32_t box[4] = {(cuuint32_t)t->shape[3], (cuuint32_t)(1 << p.box_log2), 1, 1};
+    r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, t->data, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  } else if (p.box_kind == pad::kBoxPage) {
     const cuuint64_t dims[5] = {64, 8, CB, bs / 8, (NB - 1) * p.blk_heads + H};
     const cuuint64_t strides[4] = {row, 128, 8 * row, H > 1 ? head : block};
     const cuuint32_t box[5] = {64, 8, (cuuint32_t)CB, (cuuint32_t)(1 << p.box_log2) / 8, 1};
@@ -275,23 +291,13 @@ extern "C" pad_status pad_decode_shared(const pad_tensor *q, const pad_tensor *k
     return st;
   }
   choose_box(k_cache, v_cache, pad::kSharedChunk, &p);
-  if (!fp8) {
-    if ((st = cache_map(&p.tmk, k_cache, p, "k_cache")) != PAD_OK) return st;
-    if ((st = cache_map(&p.tmv, v_cache, p, "v_cache")) != PAD_OK) return st;
-  }
+  if ((st = cache_map(&p.tmk, k_cache, p, "k_cache")) != PAD_OK) return st;
+  if ((st = cache_map(&p.tmv, v_cache, p, "v_cache")) != PAD_OK) return st;
   if ((st = query_map(&p.tmqp, q, p.gt, p.nseq)) != PAD_OK) return st;
   if ((st = query_map(&p.tmqr, q, p.gt, 1)) != PAD_OK) return st;
   p.q = static_cast<const uint16_t *>(q->data);
   p.q_sb = q->stride[0];
   p.q_sh = q->stride[1];
-  p.k = k_cache->data;
-  p.v = v_cache->data;
-  p.k_sblk = k_cache->stride[0];
-  p.k_sh = k_cache->stride[1];
-  p.k_ss = k_cache->stride[2];
-  p.v_sblk = v_cache->stride[0];
-  p.v_sh = v_cache->stride[1];
-  p.v_ss = v_cache->stride[2];
   p.shared_table = static_cast<const int32_t *>(shared_table->data);
   p.tables = static_cast<const int32_t *>(block_tables->data);
   p.table_stride = block_tables->stride[0];
