@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
       }
       ++k;
     };
-    shared_walk<D>(p, blockIdx.x, blockIdx.x == 0 ? p.cum : nullptr, [&](const SharedUnit &u) {
+    shared_walk<D>(p, blockIdx.x, [&](const SharedUnit &u) {
       put(u);
       const int box_rows = q_box_rows(u);
       const bool both = NACC == 2 && box_rows > kTileRows;
@@ -630,21 +630,47 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
 }
 
 // One warp per query row: the row's prefix units and rest units, found again
-// from the cumulative costs, weighted by their log-sum-exp.
+// from the lengths, weighted by their log-sum-exp.  What needs only the lengths is
+// done before the partial kernel has ended.
+constexpr int kMergeWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(128) shared_merge_kernel(const __grid_constant__ SharedParams p) {
+__global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __grid_constant__ SharedParams p) {
   constexpr int VEC = D / 32;
   constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.4426950408889634f;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (row >= (int64_t)p.B * p.Hq) return;
-  const int b = (int)(row / p.Hq), h = (int)(row % p.Hq);
-  const int kvh = h / p.g, ht = h % p.g / p.gt, j = h % p.g % p.gt;
-  const SharedPrefix pre = shared_prefix<D>(p);
+  __shared__ int64_t sums[2][kMergeWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per_seq = (p.Hq + kMergeWarps - 1) / kMergeWarps;
+  const int b = (int)(blockIdx.x / per_seq), h = (int)(blockIdx.x % per_seq) * kMergeWarps + warp;
+  // costs of all rest items, and of those of the sequences before b
+  int64_t all = 0, before = 0;
   bool bad;
+  for (int x = threadIdx.x; x < p.B; x += kMergeWarps * 32) {
+    const int64_t c = shared_rest_cost(p, shared_len(p, x, &bad));
+    all += c;
+    if (x < b) before += c;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    all += __shfl_xor_sync(0xffffffffu, all, off);
+    before += __shfl_xor_sync(0xffffffffu, before, off);
+  }
+  if (lane == 0) {
+    sums[0][warp] = all;
+    sums[1][warp] = before;
+  }
+  __syncthreads();
+  if (h >= p.Hq) return;
+  all = before = 0;
+#pragma unroll
+  for (int i = 0; i < kMergeWarps; ++i) {
+    all += sums[0][i];
+    before += sums[1][i];
+  }
+  const int kvh = h / p.g, ht = h % p.g / p.gt, j = h % p.g % p.gt;
+  const SharedPrefix pre = shared_prefix(p);
   const int L = shared_len(p, b, &bad), Lp = p.n_shared << p.bs_log2;
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the partials and the cumulative costs are written
-  const int64_t q = p.cum[p.B];
+  const int64_t hh = (int64_t)p.Hkv * p.HT;
+  const int64_t q = shared_div(pre.total + all * hh + p.ctas - 1, p.ctas);
 
   // An item's candidate parts: (CTA, accumulator) pairs over the CTAs that its
   // cost range touches; one that took no chunk is none.
@@ -674,14 +700,15 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const __grid_constant
               pre.chunks, ((int64_t)grp * p.nrb + rb) * p.pre_rows, p.pre_rows, rows, (b - rb * p.nseq) * p.gt + j);
   }
   if (L > Lp) {
-    const int64_t cost = shared_rest_cost<D>(p, L);
+    const int64_t cost = shared_rest_cost(p, L);
     const int k = kvh * p.HT + ht;
-    ri = make(p.cum[b] + k * cost, cost, p.w_rest, (L - Lp + kSharedChunk - 1) / kSharedChunk,
+    ri = make(pre.total + before * hh + k * cost, cost, p.w_rest, (L - Lp + kSharedChunk - 1) / kSharedChunk,
               p.rest_row0 + ((int64_t)b * p.Hkv * p.HT + k) * p.rest_rows, p.rest_rows, p.gt, j);
   }
   float m = -INFINITY, l = 0.f, acc[VEC];
 #pragma unroll
   for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the partials are written
   for (int i0 = 0; i0 < pi.n + ri.n; i0 += 32) {  // lane: one candidate
     const int i = i0 + lane;
     float s = -INFINITY;
@@ -691,7 +718,8 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const __grid_constant
       const int x = i < pi.n ? i : i - pi.n;
       const int64_t c = it.cta0 + x / it.accs;
       const int a = x % it.accs;
-      const int n = shared_cut(p, (c + 1) * q - it.start, it.w, it.chunks) - shared_cut(p, c * q - it.start, it.w, it.chunks);
+      const int n = shared_cut(p, (c + 1) * q - it.start, it.w, it.chunks) -
+                    shared_cut(p, c * q - it.start, it.w, it.chunks);
       if (a < n) {
         r = it.part + c * it.stride + a * it.rows;
         s = p.lse_part[r];
@@ -710,10 +738,11 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const __grid_constant
 #pragma unroll
     for (int x = 0; x < VEC; ++x) acc[x] *= a;
     uint32_t todo = __ballot_sync(0xffffffffu, s != -INFINITY);
-    while (todo != 0) {  // four partials in flight
-      float o[4][VEC], wj[4];
+    constexpr int kFlight = 32 / VEC < 8 ? 32 / VEC : 8;
+    while (todo != 0) {  // several partials in flight
+      float o[kFlight][VEC], wj[kFlight];
 #pragma unroll
-      for (int y = 0; y < 4; ++y) {
+      for (int y = 0; y < kFlight; ++y) {
         const int jl = todo != 0 ? __ffs(todo) - 1 : 0;
         const int64_t rj = __shfl_sync(0xffffffffu, r, jl);
         wj[y] = todo != 0 ? __shfl_sync(0xffffffffu, w, jl) : 0.f;
@@ -732,7 +761,7 @@ __global__ void __launch_bounds__(128) shared_merge_kernel(const __grid_constant
         todo &= todo - 1;
       }
 #pragma unroll
-      for (int y = 0; y < 4; ++y)
+      for (int y = 0; y < kFlight; ++y)
 #pragma unroll
         for (int x = 0; x < VEC; ++x) acc[x] += wj[y] * o[y][x];
     }
@@ -768,14 +797,13 @@ cudaError_t launch_t(const SharedParams &p, cudaStream_t s) {
   }
   shared_kernel<D, F8><<<p.ctas, C::kThreads, C::total, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int64_t rows = (int64_t)p.B * p.Hq;
   // comes up while the partial kernel's last CTAs run; waits for them before its first read
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((rows + 3) / 4));
-  cfg.blockDim = dim3(128);
+  cfg.gridDim = dim3((unsigned)p.B * (unsigned)((p.Hq + kMergeWarps - 1) / kMergeWarps));
+  cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;

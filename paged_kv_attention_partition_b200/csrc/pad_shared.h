@@ -74,7 +74,6 @@ struct SharedParams {
   float *lse_part;   // [part rows], log2 units
   int64_t rest_row0; // first part row of the rest units
   int32_t pre_rows, rest_rows;  // part rows of a prefix and a rest unit
-  int64_t *cum;      // [B + 1] cost of the rest items before sequence b (written by CTA 0)
   uint32_t *err;
 };
 

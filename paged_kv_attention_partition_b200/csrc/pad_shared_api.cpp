@@ -28,7 +28,7 @@ pad_status check_shape(const Shape &s) {
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct Layout {
-  size_t o_part, lse_part, cum, total;
+  size_t o_part, lse_part, total;
 };
 
 // Geometry and scratch of one shape: how rows are grouped into units, and room
@@ -51,10 +51,11 @@ Layout layout(const Shape &s, int ctas, pad::SharedParams *p) {
   p->max_blocks = (int32_t)s.W;
   p->bs_log2 = 0;
   while ((1ll << p->bs_log2) < s.bs) ++p->bs_log2;
-  p->w_item = 1;
-  p->w_pre1 = 2;
-  p->w_pre2 = 3;
-  p->w_rest = 2;
+  // in hundreds of cycles, from the kernel's own clocks on B200 (D = 128)
+  p->w_item = s.fp8 ? 50 : 30;
+  p->w_pre1 = s.fp8 ? 14 : 11;
+  p->w_pre2 = s.fp8 ? 26 : 24;
+  p->w_rest = s.fp8 ? 16 : 12;
   const int full = pad::shared_part_rows((int)(nseq * gt), (int)s.D);
   const int last = pad::shared_part_rows((int)((s.B - (p->nrb - 1) * nseq) * gt), (int)s.D);
   p->pre_rows = full > last ? full : last;
@@ -66,8 +67,7 @@ Layout layout(const Shape &s, int ctas, pad::SharedParams *p) {
   Layout l;
   l.o_part = 0;
   l.lse_part = align256((size_t)(rows * s.D * 4));
-  l.cum = l.lse_part + align256((size_t)(rows * 4));
-  l.total = l.cum + align256((size_t)(s.B + 1) * 8);
+  l.total = l.lse_part + align256((size_t)(rows * 4));
   return l;
 }
 
@@ -318,7 +318,6 @@ extern "C" pad_status pad_decode_shared(const pad_tensor *q, const pad_tensor *k
   char *base = static_cast<char *>(workspace);
   p.o_part = reinterpret_cast<float *>(base + l.o_part);
   p.lse_part = reinterpret_cast<float *>(base + l.lse_part);
-  p.cum = reinterpret_cast<int64_t *>(base + l.cum);
   cudaError_t e = pad::device_error_word(device, &p.err);
   if (e != cudaSuccess) return pad::host_cuda_fail(e, "error word");
   e = pad::launch_shared(p, (int)D, fp8, stream);

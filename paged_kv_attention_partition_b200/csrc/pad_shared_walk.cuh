@@ -1,5 +1,5 @@
 // Device side of the work line of pad_shared.h: the units of a CTA, and what the
-// merge needs to find a row's units again.
+// merge needs to find a row's units again (both from the lengths alone).
 #pragma once
 
 #include "pad_shared.h"
@@ -34,7 +34,6 @@ __device__ __forceinline__ int shared_len(const SharedParams &p, int b, bool *ba
 }
 
 // Cost of a rest item of a sequence of this length.
-template <int D>
 __device__ __forceinline__ int64_t shared_rest_cost(const SharedParams &p, int L) {
   const int n = L - (p.n_shared << p.bs_log2);
   return n <= 0 ? 0 : p.w_item + (int64_t)((n + kSharedChunk - 1) / kSharedChunk) * p.w_rest;
@@ -46,7 +45,6 @@ struct SharedPrefix {
   int chunks, last_nb;
   int64_t full, last, group, total;  // costs: a full block's item, the last one's, a (kvh, ht)'s, all
 };
-template <int D>
 __device__ __forceinline__ SharedPrefix shared_prefix(const SharedParams &p) {
   SharedPrefix s;
   s.chunks = ((p.n_shared << p.bs_log2) + kSharedChunk - 1) / kSharedChunk;
@@ -70,23 +68,34 @@ __device__ __forceinline__ int shared_cut(const SharedParams &p, int64_t at, int
 
 // Calls emit(unit) for each unit of CTA `cta`, in order; all lanes of a warp
 // call it together, and emit is called by all of them with the same unit.
-// cum != null: also writes the rest items' cumulative costs.
 template <int D, class Emit>
-__device__ __forceinline__ void shared_walk(const SharedParams &p, int cta, int64_t *cum, Emit &&emit) {
+__device__ __forceinline__ void shared_walk(const SharedParams &p, int cta, Emit &&emit) {
   constexpr int CT = kSharedChunk;
   const int lane = threadIdx.x & 31;
-  const SharedPrefix pre = shared_prefix<D>(p);
+  const SharedPrefix pre = shared_prefix(p);
   const int Lp = p.n_shared << p.bs_log2;
   const int hh = p.Hkv * p.HT;
+  auto length = [&](int b, bool *bad) -> int {
+    *bad = false;
+    return b < p.B ? shared_len(p, b, bad) : 0;
+  };
   int64_t sum = 0;
-  for (int b = lane; b < p.B; b += 32) {
-    bool bad;
-    sum += shared_rest_cost<D>(p, shared_len(p, b, &bad)) * hh;
-    if (bad && cta == 0 && cum != nullptr) atomicOr(p.err, kErrSeqLen);
+  bool any_bad = false;
+  for (int b = lane; b < p.B; b += 8 * 32) {  // eight loads in flight
+    int L[8];
+    bool bad[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) L[i] = length(b + 32 * i, &bad[i]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      sum += shared_rest_cost(p, L[i]);
+      any_bad |= bad[i];
+    }
   }
+  if (any_bad && cta == 0) atomicOr(p.err, kErrSeqLen);
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  const int64_t total = pre.total + sum;
+  const int64_t total = pre.total + sum * hh;
   const int64_t q = shared_div(total + p.ctas - 1, p.ctas);
   int64_t pos = cta * q;
   const int64_t end = pos + q < total ? pos + q : total;
@@ -97,7 +106,6 @@ __device__ __forceinline__ void shared_walk(const SharedParams &p, int cta, int6
     int rb = (int)shared_div(in, pre.full);
     if (rb > p.nrb - 1) rb = p.nrb - 1;
     const int64_t start = grp * pre.group + rb * pre.full;
-    const int64_t cost = rb == p.nrb - 1 ? pre.last : pre.full;
     SharedUnit u;
     u.rest = 0;
     u.kvh = grp / p.HT;
@@ -113,16 +121,16 @@ __device__ __forceinline__ void shared_walk(const SharedParams &p, int cta, int6
     u.chunks = c1 - c0;
     u.part = ((int64_t)grp * p.nrb + rb + cta) * p.pre_rows;
     if (c1 > c0) emit(u);
-    pos = start + cost;
+    pos = start + (rb == p.nrb - 1 ? pre.last : pre.full);
   }
-  if (pos >= end && cum == nullptr) return;
 
   int64_t base = pre.total;  // cost before this round's 32 sequences
-  for (int b0 = 0; b0 < p.B; b0 += 32) {
-    const int b = b0 + lane;
-    bool bad;
-    const int L = b < p.B ? shared_len(p, b, &bad) : 0;
-    const int64_t item = shared_rest_cost<D>(p, L);
+  bool bad;
+  int next = length(lane, &bad);
+  for (int b0 = 0; b0 < p.B && pos < end; b0 += 32) {
+    const int L = next;
+    next = length(b0 + 32 + lane, &bad);  // in flight during this round
+    const int64_t item = shared_rest_cost(p, L);
     int64_t incl = item * hh;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -130,10 +138,6 @@ __device__ __forceinline__ void shared_walk(const SharedParams &p, int cta, int6
       if (lane >= off) incl += o;
     }
     const int64_t first = base + incl - item * hh;
-    if (cum != nullptr && b < p.B) {
-      cum[b] = first;
-      if (b == p.B - 1) cum[p.B] = q;  // the merge needs the CTAs' share too
-    }
     uint32_t todo = __ballot_sync(0xffffffffu, item > 0 && first < end && first + item * hh > pos);
     while (todo != 0) {
       const int j = __ffs(todo) - 1;
@@ -162,7 +166,6 @@ __device__ __forceinline__ void shared_walk(const SharedParams &p, int cta, int6
       }
     }
     base += __shfl_sync(0xffffffffu, incl, 31);
-    if (cum == nullptr && base >= end) return;
   }
 }
 
