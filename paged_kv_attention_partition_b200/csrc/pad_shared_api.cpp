@@ -52,10 +52,10 @@ Layout layout(const Shape &s, int ctas, pad::SharedParams *p) {
   p->bs_log2 = 0;
   while ((1ll << p->bs_log2) < s.bs) ++p->bs_log2;
   // in hundreds of cycles, from the kernel's own clocks on B200 (D = 128)
-  p->w_item = s.fp8 ? 50 : 30;
+  p->w_item = s.fp8 ? 80 : 30;
   p->w_pre1 = s.fp8 ? 14 : 11;
-  p->w_pre2 = s.fp8 ? 26 : 24;
-  p->w_rest = s.fp8 ? 16 : 12;
+  p->w_pre2 = s.fp8 ? 26 : 20;
+  p->w_rest = s.fp8 ? 18 : 11;
   const int full = pad::shared_part_rows((int)(nseq * gt), (int)s.D);
   const int last = pad::shared_part_rows((int)((s.B - (p->nrb - 1) * nseq) * gt), (int)s.D);
   p->pre_rows = full > last ? full : last;
