@@ -315,8 +315,8 @@ pad_status pad_decode_tcgen05(const pad_tensor *q, const pad_tensor *k_cache, co
  *  q, k          bf16 [T, Hq, D] and [T, Hkv, D], last dim contiguous, rows 16-byte
  *                aligned, any other strides (slices of a fused projection); k may
  *                be NULL (then k_out and k_weight are too).
- *  q_weight,     bf16 or fp32 [D], NULL = that tensor is not normed.
- *  k_weight
+ *  q_weight,     bf16 or fp32 [D], contiguous, 16-byte aligned; NULL = that tensor
+ *  k_weight      is not normed.
  *  eps           finite, >= 0.
  *  positions     int32 [T], any values; inv_freq fp32 [R/2].  Both NULL = no rotation.
  *  q_out, k_out  bf16, the shapes of q and k, own strides; each may be its input
@@ -337,9 +337,10 @@ pad_status pad_qk_norm_rope(const pad_tensor *q, const pad_tensor *k, const pad_
  *   k_weight, eps the norm of pad_qk_norm_rope, applied to K before its rotation.
  *   q, q_weight,  query rows of the same tokens, bf16 [T, Hq, D]: normed (with
  *   q_out         q_weight and eps) and rotated into q_out by the same launch.
- *   k_scale,      an E4M3 cache holds x / scale, rounded to nearest even, beyond
- *   v_scale       +-448 as +-448, NaN as NaN.  0 reads as 1; a bf16 cache takes
- *                 0 or 1 only.  Pass the same scales to pad_decode_ex.
+ *   k_scale,      an E4M3 cache holds the fp32 quotient x / scale, rounded to nearest
+ *   v_scale       even, beyond +-448 as +-448, NaN as NaN.  0 reads as 1; otherwise in
+ *                 [2^-100, 2^100]; a bf16 cache takes 0 or 1 only.  Pass the same
+ *                 scales to pad_decode_ex.
  */
 typedef struct pad_append_options {
   const pad_tensor *inv_freq;

@@ -8,13 +8,16 @@
 // D / 16 lanes share a row: lane c holds two 16-byte chunks whose elements
 // rotate with one another (half style: chunk c of the first half and chunk c of
 // the second; neighbours: any), so the rotation needs no exchange between lanes
-// and the norm one reduction over D / 16 lanes.  A warp keeps one token, so its
-// angles are computed once for all the heads it handles.
+// and the norm one reduction over D / 16 lanes.  A warp keeps one token: its angles are
+// computed once, and weight times cosine and sine once per tensor, which leaves per
+// element a product, a multiply-add and the row's scale, two elements at a time:
+//   y1 = inv (x1 (w1 cos) + x2 (-w2 sin)),  y2 = inv (x2 (w2 cos) + x1 (w1 sin)).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
 #include "pad_device.cuh"
+#include "pad_f32x2.cuh"
 #include "pad_internal.h"
 #include "pad_rows.h"
 
@@ -23,16 +26,29 @@ namespace {
 
 constexpr int kRowsWarps = 4;
 
-__device__ __forceinline__ void unpack8(const uint4 &c, float (&x)[8]) {
+// Eight bf16 values as four pairs of fp32.
+struct Eight {
+  uint64_t p[4];
+};
+__device__ __forceinline__ Eight unpack8(const uint4 &c) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  Eight e;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) e.p[i] = duo(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+  return e;
+}
+__device__ __forceinline__ uint4 pack8(const Eight &e) {
+  uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    const float2 v = parts(e.p[i]);
+    w[i] = pack_bf16x2(v.x, v.y);
   }
+  return make_uint4(w[0], w[1], w[2], w[3]);
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ uint64_t swapped(uint64_t v) {
+  const float2 x = parts(v);
+  return duo(x.y, x.x);
 }
 // Two E4M3 codes, round to nearest even, beyond +-448 to +-448, NaN stays NaN.
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
@@ -40,13 +56,51 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
   return r;
 }
-__device__ __forceinline__ uint2 pack8_e4m3(const float (&x)[8], float scale) {
-  return make_uint2(e4m3x2(x[0] / scale, x[1] / scale) | e4m3x2(x[2] / scale, x[3] / scale) << 16,
-                    e4m3x2(x[4] / scale, x[5] / scale) | e4m3x2(x[6] / scale, x[7] / scale) << 16);
+// x / scale as E4M3 codes: the fp32 quotient, which is x * recip put right by its own
+// remainder (x / scale = q + (x - q scale) / scale; the multiply-add gives the remainder
+// exactly), rounded once more.  A product with the reciprocal alone would miss ties: 17 of
+// 3/64 comes out as 17.000002.  Values beyond the largest code are cut first, so that
+// infinities have a remainder; NaN stays NaN.  Computed as -(-q - remainder * recip):
+// that way a zero keeps its sign.
+struct CodeScale {
+  float limit;
+  uint64_t scale, minus_recip;
+};
+__device__ __forceinline__ CodeScale code_scale(float scale) {
+  const float r = 1.f / scale;
+  return {480.f * scale, duo(scale, scale), duo(-r, -r)};
 }
-__device__ __forceinline__ float weight_at(const void *w, int f32, int i) {
-  return f32 ? __ldg(static_cast<const float *>(w) + i)
-             : __uint_as_float((uint32_t)__ldg(static_cast<const uint16_t *>(w) + i) << 16);
+__device__ __forceinline__ float clip(float x, float limit) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;\n min.NaN.f32 %0, %0, %3;\n" : "=&f"(y) : "f"(x), "f"(-limit), "f"(limit));
+  return y;
+}
+__device__ __forceinline__ uint2 pack8_e4m3(const Eight &e, const CodeScale &c) {
+  uint32_t h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 v = parts(e.p[i]);
+    const uint64_t x = duo(clip(v.x, c.limit), clip(v.y, c.limit));
+    const uint64_t minus_q = mul2(x, c.minus_recip);
+    const float2 y = parts(fma2(fma2(minus_q, c.scale, x), c.minus_recip, minus_q));
+    h[i] = e4m3x2(y.x, y.y) ^ 0x8080u;
+  }
+  return make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
+}
+// Weights of a chunk; ones without.
+__device__ __forceinline__ Eight weights8(const void *w, int f32, int chunk) {
+  Eight e;
+  if (w == nullptr) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) e.p[i] = duo(1.f, 1.f);
+  } else if (f32) {
+    const float4 *p = static_cast<const float4 *>(w) + 2 * chunk;
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    e.p[0] = duo(a.x, a.y), e.p[1] = duo(a.z, a.w), e.p[2] = duo(b.x, b.y), e.p[3] = duo(b.z, b.w);
+  } else {
+    e = unpack8(__ldg(static_cast<const uint4 *>(w) + chunk));
+  }
+  return e;
 }
 // cos and sin of position * freq.  The product and its reduction to half turns
 // are in 64 bits: in 32 a position of 10^5 alone would lose the angle's last two
@@ -57,123 +111,199 @@ __device__ __forceinline__ void angle(int pos, float freq, float &c, float &s) {
   sincospif((float)half_turns, &s, &c);
 }
 
-template <int D, int MODE>
-__global__ void __launch_bounds__(kRowsWarps * 32) rows_kernel(const __grid_constant__ RowsParams p) {
+// One tensor's part of the warp's steps: lane's row of its first step, where it goes,
+// and how far from there to the next step's.
+struct Segment {
+  char *dst;        // null: nowhere
+  int64_t dstep;    // bytes
+  int steps, rows;  // steps, and rows from this lane's first one on (a lane past the last has none)
+};
+
+template <int D, int MODE, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRowsWarps * 32, 5) rows_kernel(const __grid_constant__ RowsParams p) {
   constexpr int LPR = D / 16, RPW = 32 / LPR;  // lanes per row, rows per warp step
-  constexpr bool kCache = MODE != kRowsOut;
-  const int lane = threadIdx.x & 31, c = lane % LPR, sub = lane / LPR;
-  const int rows = p.Hq + p.Hkv * (kCache ? 2 : 1);
-  const int steps = (rows + RPW - 1) / RPW;
-  const int parts = (steps + p.steps_per_warp - 1) / p.steps_per_warp;
-  const int64_t w = (int64_t)blockIdx.x * kRowsWarps + (threadIdx.x >> 5);
-  const int64_t t = w / parts;
+  constexpr bool kCache = MODE != kRowsOut, kCodes = MODE == kRowsCacheE4m3;
+  constexpr int kHeld = kCodes ? 1 : 2;  // bytes of a cached element
+  __shared__ float2 turns[kRowsWarps][D / 2];  // cos, sin of the warp's token
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LPR, sub = lane / LPR;
+  const int nq = (p.Hq + RPW - 1) / RPW, nk = (p.Hkv + RPW - 1) / RPW, steps = nq + nk * (kCache ? 2 : 1);
+  const int share = (steps + p.steps_per_warp - 1) / p.steps_per_warp;
+  const int64_t w = (int64_t)blockIdx.x * kRowsWarps + warp;
+  const int64_t t = w / share;
   if (t >= p.T) return;
-  const int s0 = (int)(w % parts) * p.steps_per_warp, s1 = min(s0 + p.steps_per_warp, steps);
+  const int s0 = (int)(w - t * share) * p.steps_per_warp, s1 = min(s0 + p.steps_per_warp, steps);
+  // the warp's steps of q, k and v: [from, to) of each one's own
+  const int q0 = min(s0, nq), q1 = min(s1, nq);
+  const int k0 = min(max(s0 - nq, 0), nk), k1 = min(max(s1 - nq, 0), nk);
+  const int v0 = max(s0 - nq - nk, 0), v1 = max(s1 - nq - nk, 0);
 
   // this lane's chunks: a rotating pair (half style), or two neighbours
   const int hc = p.inv_freq != nullptr ? p.rot / 16 : 0;  // rotating chunk pairs
   const bool turn = c < hc;
-  int c0 = 2 * c, c1 = 2 * c + 1;
-  if (turn && !p.interleaved) {
-    c0 = c;
-    c1 = c + hc;
-  }
-  float cs[8], sn[8];
-  if (turn) {
-    const int pos = __ldg(p.positions + t);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) angle(pos, __ldg(p.inv_freq + 8 * c + i), cs[i], sn[i]);
-  }
-  // where the token goes; block < 0: nowhere
-  int block = -1, slot = 0;
-  if (kCache) {
-    const int seq = p.seq_ids != nullptr ? __ldg(p.seq_ids + t) : (int)t;
-    if (seq >= 0) {
-      const int pos = __ldg(p.positions + t);
-      const bool seq_ok = seq < p.B, pos_ok = pos >= 0 && (pos >> p.bs_log2) < p.max_blocks;
-      if (seq_ok && pos_ok) {
-        block = __ldg(p.tables + seq * p.table_stride + (pos >> p.bs_log2));
-        slot = pos & ((1 << p.bs_log2) - 1);
-      }
-      if (block < 0 || block >= p.num_blocks) {
-        if (lane == 0) atomicOr(p.err, seq_ok && !pos_ok ? kErrSeqLen : kErrBlockId);
-        block = -1;
-      }
+  const bool apart = turn && !INTERLEAVED;
+  const int c0 = apart ? c : 2 * c, c1 = apart ? c + hc : 2 * c + 1;
+
+  // The rows in order, q's, k's, v's, fetched two steps ahead: the first two before
+  // anything that waits for another load.
+  const uint16_t *src;
+  int64_t sstep;
+  int left, rows;   // steps and rows of the tensor being fetched
+  int tensor = -1;  // 0 q, 1 k, 2 v
+  auto next_tensor = [&]() {
+    for (left = 0; left == 0 && tensor < 2;) {
+      ++tensor;
+      const int a = tensor == 0 ? q0 : tensor == 1 ? k0 : v0;
+      left = (tensor == 0 ? q1 : tensor == 1 ? k1 : v1) - a;
+      const int64_t sh = tensor == 0 ? p.q_sh : tensor == 1 ? p.k_sh : p.v_sh;
+      const int h = a * RPW + sub;
+      rows = (tensor == 0 ? p.Hq : p.Hkv) - h;
+      sstep = sh * RPW;
+      src = (tensor == 0 ? p.q + t * p.q_st : tensor == 1 ? p.k + t * p.k_st : p.v + t * p.v_st) + h * sh + c0 * 8;
     }
+  };
+  const int delta = (c1 - c0) * 8;
+  auto fetch = [&](uint4 &a, uint4 &b) {
+    a = b = make_uint4(0, 0, 0, 0);
+    if (left == 0) return;
+    if (rows > 0) {
+      a = *reinterpret_cast<const uint4 *>(src);
+      b = *reinterpret_cast<const uint4 *>(src + delta);
+    }
+    src += sstep;
+    rows -= RPW;
+    if (--left == 0) next_tensor();
+  };
+  next_tensor();
+  uint4 na[2], nb[2];
+  fetch(na[0], nb[0]);
+  fetch(na[1], nb[1]);
+
+  const bool turns_any = hc > 0 && s0 < nq + nk, caches = kCache && s1 > nq;  // (V alone needs no angles)
+  const int pos = turns_any || caches ? __ldg(p.positions + t) : 0;
+  const int seq = !caches ? -1 : p.seq_ids != nullptr ? __ldg(p.seq_ids + t) : (int)t;
+  // where the token goes; block < 0: nowhere
+  int block = -1;
+  if (seq >= 0) {
+    const bool seq_ok = seq < p.B, pos_ok = pos >= 0 && (pos >> p.bs_log2) < p.max_blocks;
+    if (seq_ok && pos_ok) block = __ldg(p.tables + seq * p.table_stride + (pos >> p.bs_log2));
+    if (block < 0 || block >= p.num_blocks) {
+      if (lane == 0) atomicOr(p.err, seq_ok && !pos_ok ? kErrSeqLen : kErrBlockId);
+      block = -1;
+    }
+  }
+  const int slot = pos & ((1 << p.bs_log2) - 1);
+  // the token's angles, shared out over the warp
+  if (turns_any) {
+    for (int i = lane; i < p.rot / 2; i += 32) angle(pos, __ldg(p.inv_freq + i), turns[warp][i].x, turns[warp][i].y);
+    __syncwarp();
   }
 
-  for (int st = s0; st < s1; ++st) {
-    const int r = st * RPW + sub;
-    const bool live = r < rows;
-    const bool is_q = r < p.Hq, is_v = r >= p.Hq + p.Hkv;
-    const int h = is_q ? r : is_v ? r - p.Hq - p.Hkv : r - p.Hq;
-    const uint16_t *src = is_q ? p.q + t * p.q_st + h * p.q_sh
-                               : is_v ? p.v + t * p.v_st + h * p.v_sh : p.k + t * p.k_st + h * p.k_sh;
-    float x[8], y[8];
-    float ss = 0.f;
-    if (live) {
-      unpack8(*reinterpret_cast<const uint4 *>(src + c0 * 8), x);
-      unpack8(*reinterpret_cast<const uint4 *>(src + c1 * 8), y);
+  // weights: the tensor's norm; null: none.
+  auto run = [&](const Segment &g, bool codes, float scale, bool rotates, const void *weights, int f32) {
+    if (g.steps <= 0) return;
+    const bool spin = turn && rotates;
+    // coefficients: of the chunks themselves, and of the elements that turn into them
+    Eight wa = weights8(weights, f32, c0), wb = weights8(weights, f32, c1), ua{}, ub{};
+    if (spin) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) ss += x[i] * x[i] + y[i] * y[i];
-    }
-#pragma unroll
-    for (int off = LPR / 2; off > 0; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-    if (!live) continue;
-    const void *wt = is_q ? p.qw : is_v ? nullptr : p.kw;
-    if (wt != nullptr) {
-      const float inv = rsqrtf(ss * (1.f / D) + p.eps);
-      const int f32 = is_q ? p.qw_f32 : p.kw_f32;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        x[i] *= inv * weight_at(wt, f32, c0 * 8 + i);
-        y[i] *= inv * weight_at(wt, f32, c1 * 8 + i);
+      for (int i = 0; i < 4; ++i) {
+        const float2 a = parts(wa.p[i]), b = parts(wb.p[i]);
+        if constexpr (INTERLEAVED) {
+          const float2 x = turns[warp][8 * c + i], y = turns[warp][8 * c + 4 + i];
+          wa.p[i] = duo(a.x * x.x, a.y * x.x);
+          ua.p[i] = duo(-a.y * x.y, a.x * x.y);
+          wb.p[i] = duo(b.x * y.x, b.y * y.x);
+          ub.p[i] = duo(-b.y * y.y, b.x * y.y);
+        } else {
+          const float2 x = turns[warp][8 * c + 2 * i], y = turns[warp][8 * c + 2 * i + 1];
+          wa.p[i] = duo(a.x * x.x, a.y * y.x);
+          ua.p[i] = duo(-b.x * x.y, -b.y * y.y);
+          wb.p[i] = duo(b.x * x.x, b.y * y.x);
+          ub.p[i] = duo(a.x * x.y, a.y * y.y);
+        }
       }
     }
-    if (turn && !is_v) {
-      if (p.interleaved) {
+    CodeScale cs{};
+    if constexpr (kCodes) cs = code_scale(scale);
+    char *dst = g.dst;
+    int rows_left = g.dst == nullptr ? 0 : g.rows;
+    for (int st = 0; st < g.steps; ++st, dst += g.dstep, rows_left -= RPW) {
+      const uint4 ra = na[0], rb = nb[0];
+      na[0] = na[1];
+      nb[0] = nb[1];
+      fetch(na[1], nb[1]);
+      if (weights == nullptr && !rotates && !codes) {  // as it is, bit for bit
+        if (rows_left > 0) {
+          *reinterpret_cast<uint4 *>(dst + c0 * 16) = ra;
+          *reinterpret_cast<uint4 *>(dst + c1 * 16) = rb;
+        }
+        continue;
+      }
+      Eight a = unpack8(ra), b = unpack8(rb);
+      float inv = 1.f;
+      if (weights != nullptr) {
+        uint64_t ss[2] = {0, 0};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float x1 = x[2 * i], x2 = x[2 * i + 1], y1 = y[2 * i], y2 = y[2 * i + 1];
-          x[2 * i] = x1 * cs[i] - x2 * sn[i];
-          x[2 * i + 1] = x2 * cs[i] + x1 * sn[i];
-          y[2 * i] = y1 * cs[4 + i] - y2 * sn[4 + i];
-          y[2 * i + 1] = y2 * cs[4 + i] + y1 * sn[4 + i];
+          ss[0] = fma2(a.p[i], a.p[i], ss[0]);
+          ss[1] = fma2(b.p[i], b.p[i], ss[1]);
         }
-      } else {
+        const float2 s2 = parts(add2(ss[0], ss[1]));
+        float s = s2.x + s2.y;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float x1 = x[i], x2 = y[i];
-          x[i] = x1 * cs[i] - x2 * sn[i];
-          y[i] = x2 * cs[i] + x1 * sn[i];
+        for (int off = LPR / 2; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+        inv = rsqrtf(s * (1.f / D) + p.eps);
+      }
+      if (rows_left <= 0) continue;
+      const uint64_t inv2 = duo(inv, inv);
+      if (spin) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t x = fma2(INTERLEAVED ? swapped(a.p[i]) : b.p[i], ua.p[i], mul2(a.p[i], wa.p[i]));
+          const uint64_t y = fma2(INTERLEAVED ? swapped(b.p[i]) : a.p[i], ub.p[i], mul2(b.p[i], wb.p[i]));
+          a.p[i] = mul2(x, inv2);
+          b.p[i] = mul2(y, inv2);
+        }
+      } else if (weights != nullptr) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a.p[i] = mul2(mul2(a.p[i], wa.p[i]), inv2);
+          b.p[i] = mul2(mul2(b.p[i], wb.p[i]), inv2);
         }
       }
-    }
-    if (is_q || !kCache) {
-      uint16_t *o = is_q ? p.q_out + t * p.qo_st + h * p.qo_sh : p.k_out + t * p.ko_st + h * p.ko_sh;
-      *reinterpret_cast<uint4 *>(o + c0 * 8) = pack8(x);
-      *reinterpret_cast<uint4 *>(o + c1 * 8) = pack8(y);
-    } else if (block >= 0) {
-      const int64_t at = is_v ? block * p.vc_sb + h * p.vc_sh + slot * p.vc_ss
-                              : block * p.kc_sb + h * p.kc_sh + slot * p.kc_ss;
-      if constexpr (MODE == kRowsCacheE4m3) {
-        uint8_t *o = static_cast<uint8_t *>(is_v ? p.vc : p.kc) + at;
-        const float sc = is_v ? p.v_scale : p.k_scale;
-        *reinterpret_cast<uint2 *>(o + c0 * 8) = pack8_e4m3(x, sc);
-        *reinterpret_cast<uint2 *>(o + c1 * 8) = pack8_e4m3(y, sc);
+      if (kCodes && codes) {
+        *reinterpret_cast<uint2 *>(dst + c0 * 8) = pack8_e4m3(a, cs);
+        *reinterpret_cast<uint2 *>(dst + c1 * 8) = pack8_e4m3(b, cs);
       } else {
-        uint16_t *o = static_cast<uint16_t *>(is_v ? p.vc : p.kc) + at;
-        *reinterpret_cast<uint4 *>(o + c0 * 8) = pack8(x);
-        *reinterpret_cast<uint4 *>(o + c1 * 8) = pack8(y);
+        *reinterpret_cast<uint4 *>(dst + c0 * 16) = pack8(a);
+        *reinterpret_cast<uint4 *>(dst + c1 * 16) = pack8(b);
       }
     }
+  };
+  // from, to: steps; head 0's destination and the bytes from head to head
+  auto segment = [&](char *dst, int64_t dsh, int heads, int from, int to) -> Segment {
+    const int h = from * RPW + sub;
+    return {dst == nullptr ? nullptr : dst + h * dsh, dsh * RPW, to - from, heads - h};
+  };
+  run(segment(reinterpret_cast<char *>(p.q_out + t * p.qo_st), p.qo_sh * 2, p.Hq, q0, q1), false, 1.f, hc > 0, p.qw,
+      p.qw_f32);
+  if constexpr (kCache) {
+    char *kd = block < 0 ? nullptr
+                         : static_cast<char *>(p.kc) + ((int64_t)block * p.kc_sb + (int64_t)slot * p.kc_ss) * kHeld;
+    run(segment(kd, p.kc_sh * kHeld, p.Hkv, k0, k1), kCodes, p.k_scale, hc > 0, p.kw, p.kw_f32);
+    char *vd = block < 0 ? nullptr
+                         : static_cast<char *>(p.vc) + ((int64_t)block * p.vc_sb + (int64_t)slot * p.vc_ss) * kHeld;
+    run(segment(vd, p.vc_sh * kHeld, p.Hkv, v0, v1), kCodes, p.v_scale, false, nullptr, 0);
+  } else {
+    run(segment(reinterpret_cast<char *>(p.k_out + t * p.ko_st), p.ko_sh * 2, p.Hkv, k0, k1), false, 1.f, hc > 0, p.kw,
+        p.kw_f32);
   }
 }
 
 template <int D, int MODE>
 cudaError_t launch_t(RowsParams p, int sms, cudaStream_t s) {
   constexpr int RPW = 32 / (D / 16);
-  const int rows = p.Hq + p.Hkv * (MODE != kRowsOut ? 2 : 1), steps = (rows + RPW - 1) / RPW;
+  const int steps = (p.Hq + RPW - 1) / RPW + (p.Hkv + RPW - 1) / RPW * (MODE != kRowsOut ? 2 : 1);
   // One step per warp while the launch has room for it (latency), then as many
   // of a token's heads per warp as keep every SM at 16 warps: each further step
   // reuses the warp's angles.
@@ -182,7 +312,8 @@ cudaError_t launch_t(RowsParams p, int sms, cudaStream_t s) {
   const int64_t warps = p.T * ((steps + p.steps_per_warp - 1) / p.steps_per_warp);
   const int64_t grid = (warps + kRowsWarps - 1) / kRowsWarps;
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-  rows_kernel<D, MODE><<<(unsigned)grid, kRowsWarps * 32, 0, s>>>(p);
+  if (p.interleaved) rows_kernel<D, MODE, true><<<(unsigned)grid, kRowsWarps * 32, 0, s>>>(p);
+  else rows_kernel<D, MODE, false><<<(unsigned)grid, kRowsWarps * 32, 0, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -67,7 +67,12 @@ pad_status check_vector(const pad_tensor *t, const char *name, pad_dtype dt, int
 }
 
 pad_status check_weight(const pad_tensor *t, const char *name, int64_t D) {
-  return t == nullptr ? PAD_OK : check_vector(t, name, t->dtype == PAD_F32 ? PAD_F32 : PAD_BF16, D);
+  if (t == nullptr) return PAD_OK;
+  pad_status st = check_vector(t, name, t->dtype == PAD_F32 ? PAD_F32 : PAD_BF16, D);
+  if (st != PAD_OK) return st;
+  if (reinterpret_cast<uintptr_t>(t->data) % 16)
+    return host_fail(PAD_ERR_INVALID_ARG, "%s: data must be 16-byte aligned", name);
+  return PAD_OK;
 }
 
 pad_status check_rotation(const pad_tensor *inv_freq, int64_t D) {
@@ -241,6 +246,9 @@ extern "C" pad_status pad_append_kv(const pad_tensor *k, const pad_tensor *v, co
     return host_fail(PAD_ERR_INVALID_ARG, "k_scale and v_scale must be finite and positive (or 0 for 1)");
   if (!fp8 && (k_scale != 1.f || v_scale != 1.f))
     return host_fail(PAD_ERR_INVALID_ARG, "k_scale / v_scale apply to an E4M3 cache only (bf16 cache: 0 or 1)");
+  for (float s : {k_scale, v_scale})
+    if (s < 0x1p-100f || s > 0x1p100f)
+      return host_fail(PAD_ERR_UNSUPPORTED, "scale %g outside [2^-100, 2^100]", (double)s);
   if (T == 0) return PAD_OK;
 
   int device = 0;
