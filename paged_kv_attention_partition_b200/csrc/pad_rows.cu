@@ -304,11 +304,20 @@ template <int D, int MODE>
 cudaError_t launch_t(RowsParams p, int sms, cudaStream_t s) {
   constexpr int RPW = 32 / (D / 16);
   const int steps = (p.Hq + RPW - 1) / RPW + (p.Hkv + RPW - 1) / RPW * (MODE != kRowsOut ? 2 : 1);
-  // One step per warp while the launch has room for it (latency), then as many
-  // of a token's heads per warp as keep every SM at 16 warps: each further step
-  // reuses the warp's angles.
-  int64_t spw = p.T * steps / ((int64_t)sms * 16);
-  p.steps_per_warp = (int)(spw < 1 ? 1 : spw > steps ? steps : spw);
+  // Steps of a warp: the fewest rounds of resident warps, each as long as a warp's
+  // steps and its start (angles and place: about four steps).  A step's token gets one warp per
+  // step (16 heads of 8 tokens: 3.2 us); 2001 tokens of 10 steps one warp each, one round
+  // (12.1 us; two warps each, two rounds, 15.3 us).
+  const int64_t slots = (int64_t)sms * 5 * kRowsWarps;
+  int64_t best = -1;
+  for (int n = 1; n <= steps; ++n) {
+    const int64_t rounds = (p.T * ((steps + n - 1) / n) + slots - 1) / slots, cost = rounds * (n + 4);
+    if (best < 0 || cost < best) {
+      best = cost;
+      p.steps_per_warp = n;
+    }
+    if (n >= 256) n += n / 16;  // (thousands of heads: no need to try every one)
+  }
   const int64_t warps = p.T * ((steps + p.steps_per_warp - 1) / p.steps_per_warp);
   const int64_t grid = (warps + kRowsWarps - 1) / kRowsWarps;
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
