@@ -84,16 +84,16 @@ struct SharedCfg {
 };
 static_assert(sizeof(SharedUnit) <= 64, "queue entry");
 
-// Power of two that scales a row of bf16 q whose largest magnitude has these bits
+// Power of two that scales a row of bf16 q whose largest magnitude is that of either half
 // into f16's range, as an exponent; 0 for a row of zeros or one that is not finite.
-__device__ __forceinline__ int q_exponent(uint32_t abs_bits) {
+__device__ __forceinline__ int q_exponent(uint32_t halves) {
+  const uint32_t abs_bits = max(halves & 0xffffu, halves >> 16);
   return abs_bits == 0 || abs_bits >= 0x7f80u ? 0 : min(100, max(-100, 141 - (int)(abs_bits >> 7)));
 }
+// Largest magnitudes of the even and of the odd values so far, a half each.
 __device__ __forceinline__ uint32_t max_abs(uint32_t m, const uint4 &c) {
-  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) m = max(m, max(w[i] & 0x7fffu, w[i] >> 16 & 0x7fffu));
-  return m;
+  const uint32_t k = 0x7fff7fffu;
+  return __vmaxu2(m, __vmaxu2(__vmaxu2(c.x & k, c.y & k), __vmaxu2(c.z & k, c.w & k)));
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }
 
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
       mbar_init(empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + 8 * i, F8 ? 2 : 1);
+      mbar_init(q_full + 8 * i, F8 ? 4 : 1);  // the widening warps, or the copy
       if (F8) mbar_init(q_tx + 8 * i, 1);
       mbar_init(q_empty + 8 * i, 1);
       mbar_init(o_free + 8 * i, C::kGroupWarps);
@@ -401,29 +401,34 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
     auto all = [&](bool v) { return __all_sync(0xffffffffu, v) != 0; };
     SharedUnit u;
     for (int k = 0; ok && (ok = next_unit(k, u)) && u.chunks > 0; ++k) {
-      if (is_k) {  // ---- q: bf16 to f16 in place, a thread per row
+      {  // ---- q: bf16 to f16 in place, by both rings' warps
         const bool both = NACC == 2 && q_box_rows(u) > kTileRows;
         const int h = both || NACC == 1 ? 0 : half;
         if (!both && NACC == 2) half ^= 1;
         ok = all(wait(q_tx + 8 * h, qphase >> h & 1)) && (!both || all(wait(q_tx + 8, qphase >> 1)));
         if (!ok) break;
         qphase ^= both ? 3 : 1 << h;
-        for (int r = t; r < u.rows; r += 64) {
-          uint8_t *row = smem + (h * kTileRows + r) * 128;
-          uint32_t m = 0;
+        // 16 bytes of a row per lane: a thread per row would take a rest unit, with its
+        // few rows, as long as a full tile.
+        constexpr int QL = D / 8, RI = 32 / QL, kRows = 4;  // lanes of a row; rows of a warp at a time, times kRows in flight
+        const int c = lane % QL;
+        for (int r0 = (warp - C::kWidenWarp) * RI + lane / QL; r0 - lane / QL < u.rows; r0 += 4 * RI * kRows) {
+          uint4 v[kRows];
+          auto at = [&](int i) {
+            const int r = r0 + i * 4 * RI;
+            return reinterpret_cast<uint4 *>(smem + (h * kTileRows + r) * 128 + (c >> 3) * C::kQBlock + ((c ^ r) & 7) * 16);
+          };
 #pragma unroll
-          for (int c = 0; c < CB * 8; ++c)
-            m = max_abs(m, *reinterpret_cast<const uint4 *>(row + (c >> 3) * C::kQBlock + ((c ^ r) & 7) * 16));
-          const float f = pow2(q_exponent(m));
+          for (int i = 0; i < kRows; ++i) v[i] = r0 + i * 4 * RI < u.rows ? *at(i) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-          for (int c = 0; c < CB * 8; ++c) {
-            uint32_t *x = reinterpret_cast<uint32_t *>(row + (c >> 3) * C::kQBlock + ((c ^ r) & 7) * 16);
-            uint4 v = *reinterpret_cast<const uint4 *>(x);
-            v.x = pack_f16x2(__uint_as_float(v.x << 16) * f, __uint_as_float(v.x & 0xffff0000u) * f);
-            v.y = pack_f16x2(__uint_as_float(v.y << 16) * f, __uint_as_float(v.y & 0xffff0000u) * f);
-            v.z = pack_f16x2(__uint_as_float(v.z << 16) * f, __uint_as_float(v.z & 0xffff0000u) * f);
-            v.w = pack_f16x2(__uint_as_float(v.w << 16) * f, __uint_as_float(v.w & 0xffff0000u) * f);
-            *reinterpret_cast<uint4 *>(x) = v;
+          for (int i = 0; i < kRows; ++i) {
+            if (r0 - lane / QL + i * 4 * RI >= u.rows) break;
+            uint32_t m = max_abs(0, v[i]);
+#pragma unroll
+            for (int off = QL / 2; off > 0; off >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
+            const float f = pow2(q_exponent(m));
+            auto scaled = [&](uint32_t x) { return pack_f16x2(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f); };
+            if (r0 + i * 4 * RI < u.rows) *at(i) = make_uint4(scaled(v[i].x), scaled(v[i].y), scaled(v[i].z), scaled(v[i].w));
           }
         }
         fence_proxy_async_smem();
@@ -441,21 +446,30 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
         uint8_t *to = smem + C::ring + s * C::kSlot;
         const int nv = is_k ? CT : u.tok1 - (u.tok0 + c * CT);  // V: zeros behind the unit's tokens
         const int in_box = (1 << p.box_log2) - 1;
+        constexpr int kFlight = LR < 8 ? LR : 8;  // loads in flight, all before the first store
 #pragma unroll
-        for (int i = 0; i < LR; ++i) {
-          const int row = i * (64 / LR) + t / LR, x = t % LR;
-          const uint4 v = row < nv ? *reinterpret_cast<const uint4 *>(raw + (row >> p.box_log2) * p.box_pitch +
-                                                                      (row & in_box) * D + x * 16)
-                                   : make_uint4(0, 0, 0, 0);
-          uint4 a, b;  // codes 0-7 and 8-15
-          e4m3x4_to_f16x2x2(v.x, a.x, a.y);
-          e4m3x4_to_f16x2x2(v.y, a.z, a.w);
-          e4m3x4_to_f16x2x2(v.z, b.x, b.y);
-          e4m3x4_to_f16x2x2(v.w, b.z, b.w);
-          uint8_t *d = to + (row >> 3) * C::kGroup + (x >> 2) * 1024 + (row & 7) * 128;
-          const int c0 = (2 * (x & 3)) ^ (row & 7), odd = x >> 2 & 1;  // odd blocks store their second chunk first:
-          *reinterpret_cast<uint4 *>(d + (c0 ^ odd) * 16) = odd ? b : a;  // eight threads, eight 16-byte banks
-          *reinterpret_cast<uint4 *>(d + (c0 ^ odd ^ 1) * 16) = odd ? a : b;
+        for (int i0 = 0; i0 < LR; i0 += kFlight) {
+          uint4 code[kFlight];
+#pragma unroll
+          for (int i = 0; i < kFlight; ++i) {
+            const int row = (i0 + i) * (64 / LR) + t / LR, x = t % LR;
+            code[i] = row < nv ? *reinterpret_cast<const uint4 *>(raw + (row >> p.box_log2) * p.box_pitch +
+                                                                  (row & in_box) * D + x * 16)
+                               : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+          for (int i = 0; i < kFlight; ++i) {
+            const int row = (i0 + i) * (64 / LR) + t / LR, x = t % LR;
+            uint4 a, b;  // codes 0-7 and 8-15
+            e4m3x4_to_f16x2x2(code[i].x, a.x, a.y);
+            e4m3x4_to_f16x2x2(code[i].y, a.z, a.w);
+            e4m3x4_to_f16x2x2(code[i].z, b.x, b.y);
+            e4m3x4_to_f16x2x2(code[i].w, b.z, b.w);
+            uint8_t *d = to + (row >> 3) * C::kGroup + (x >> 2) * 1024 + (row & 7) * 128;
+            const int c0 = (2 * (x & 3)) ^ (row & 7), odd = x >> 2 & 1;  // odd blocks store their second chunk first:
+            *reinterpret_cast<uint4 *>(d + (c0 ^ odd) * 16) = odd ? b : a;  // eight threads, eight 16-byte banks
+            *reinterpret_cast<uint4 *>(d + (c0 ^ odd ^ 1) * 16) = odd ? a : b;
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
