@@ -75,9 +75,10 @@ struct SharedCfg {
   static constexpr int kSoftmaxWarps = kGroupWarps * NACC;
   static constexpr int kKWarp = kSoftmaxWarps, kVWarp = kSoftmaxWarps + 1, kQkWarp = kSoftmaxWarps + 2,
                        kPvWarp = kSoftmaxWarps + 3, kWidenWarp = kSoftmaxWarps + 4,
-                       kUnitWarp = kSoftmaxWarps + (F8 ? 8 : 4);
+                       kUnitWarp = kSoftmaxWarps + (F8 ? 12 : 4);
   static constexpr int kWarps = kUnitWarp + 1, kThreads = kWarps * 32;
-  static constexpr uint32_t ring = kQ, raw = ring + NS * kSlot, queue = raw + 2 * NR * kRaw,
+  static constexpr uint32_t ring = kQ, raw = ring + NS * kSlot, unscale = raw + 2 * NR * kRaw,
+                            queue = unscale + (F8 ? QR * 4 : 0),
                             bars = queue + kQueue * 64;
   static constexpr uint32_t kBarBytes = 640, total = bars + kBarBytes + 1024 /* alignment slack */;
   static constexpr uint32_t kSCol = CT, kOCol = NBUF * CT;  // tensor memory: S buffers, then O
@@ -108,6 +109,7 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sq = smem_addr(smem), sring = sq + C::ring;
   SharedUnit *queue = reinterpret_cast<SharedUnit *>(smem + C::queue);  // entries 64 bytes apart
+  float *unscale = reinterpret_cast<float *>(smem + C::unscale);  // E4M3: 1 / the power of two of each q row
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::bars);
   const uint32_t bar0 = smem_addr(bars);
   const uint32_t full = bar0, empty = full + 8 * NS, q_full = empty + 8 * NS, q_empty = q_full + 16,
@@ -123,13 +125,13 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
 
   if (tid == 0) {
     for (int i = 0; i < NS; ++i) {
-      mbar_init(full + 8 * i, F8 ? 2 : 1);  // a ring's widening warps, or the copy
+      mbar_init(full + 8 * i, F8 ? 4 : 1);  // a ring's widening warps, or the copy
       mbar_init(empty + 8 * i, 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full + 8 * i, F8 ? 4 : 1);  // the widening warps, or the copy
+      mbar_init(q_full + 8 * i, F8 ? 8 : 1);  // the widening warps, or the copy
       if (F8) mbar_init(q_tx + 8 * i, 1);
-      mbar_init(q_empty + 8 * i, 1);
+      mbar_init(q_empty + 8 * i, F8 ? 1 + C::kSoftmaxWarps : 1);  // its products; E4M3: and its rows' powers read
       mbar_init(o_free + 8 * i, C::kGroupWarps);
     }
     for (int i = 0; i < NBUF; ++i) {
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
     }
     for (int i = 0; i < 2 * C::NR; ++i) {
       mbar_init(raw_full + 8 * i, 1);
-      mbar_init(raw_empty + 8 * i, 2);
+      mbar_init(raw_empty + 8 * i, 4);
     }
     mbar_init(idle, 2);
     *abort_flag = 0;
@@ -391,8 +393,8 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
     }
     if (tc::elect()) tc::commit(idle);
   } else if (F8 && warp >= C::kWidenWarp) {
-    const bool is_k = warp < C::kWidenWarp + 2;
-    const int t = (warp & 1) * 32 + lane;  // (kWidenWarp is even) of the ring's 64 threads
+    const bool is_k = warp < C::kWidenWarp + 4;
+    const int t = (warp & 3) * 32 + lane;  // (kWidenWarp is a multiple of 4) of the ring's 128 threads
     constexpr int LR = D / 16;             // threads of a row: 16 codes each
     const uint32_t first = is_k ? 0 : C::NK, slots = is_k ? C::NK : C::NV, raw0 = is_k ? 0 : C::NR;
     uint32_t slot = 0, phase = 1, rslot = 0, rphase = 0, qphase = 0;
@@ -410,25 +412,26 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
         qphase ^= both ? 3 : 1 << h;
         // 16 bytes of a row per lane: a thread per row would take a rest unit, with its
         // few rows, as long as a full tile.
-        constexpr int QL = D / 8, RI = 32 / QL, kRows = 4;  // lanes of a row; rows of a warp at a time, times kRows in flight
+        constexpr int QL = D / 8, RI = 32 / QL, kRows = 2;  // lanes of a row; rows of a warp at a time, times kRows in flight
         const int c = lane % QL;
-        for (int r0 = (warp - C::kWidenWarp) * RI + lane / QL; r0 - lane / QL < u.rows; r0 += 4 * RI * kRows) {
+        for (int r0 = (warp - C::kWidenWarp) * RI + lane / QL; r0 - lane / QL < u.rows; r0 += 8 * RI * kRows) {
           uint4 v[kRows];
           auto at = [&](int i) {
-            const int r = r0 + i * 4 * RI;
+            const int r = r0 + i * 8 * RI;
             return reinterpret_cast<uint4 *>(smem + (h * kTileRows + r) * 128 + (c >> 3) * C::kQBlock + ((c ^ r) & 7) * 16);
           };
 #pragma unroll
-          for (int i = 0; i < kRows; ++i) v[i] = r0 + i * 4 * RI < u.rows ? *at(i) : make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < kRows; ++i) v[i] = r0 + i * 8 * RI < u.rows ? *at(i) : make_uint4(0, 0, 0, 0);
 #pragma unroll
           for (int i = 0; i < kRows; ++i) {
-            if (r0 - lane / QL + i * 4 * RI >= u.rows) break;
+            if (r0 - lane / QL + i * 8 * RI >= u.rows) break;
             uint32_t m = max_abs(0, v[i]);
 #pragma unroll
             for (int off = QL / 2; off > 0; off >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
             const float f = pow2(q_exponent(m));
             auto scaled = [&](uint32_t x) { return pack_f16x2(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f); };
-            if (r0 + i * 4 * RI < u.rows) *at(i) = make_uint4(scaled(v[i].x), scaled(v[i].y), scaled(v[i].z), scaled(v[i].w));
+            if (c == 0 && r0 + i * 8 * RI < u.rows) unscale[h * kTileRows + r0 + i * 8 * RI] = pow2(-q_exponent(m));
+            if (r0 + i * 8 * RI < u.rows) *at(i) = make_uint4(scaled(v[i].x), scaled(v[i].y), scaled(v[i].z), scaled(v[i].w));
           }
         }
         fence_proxy_async_smem();
@@ -446,20 +449,20 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
         uint8_t *to = smem + C::ring + s * C::kSlot;
         const int nv = is_k ? CT : u.tok1 - (u.tok0 + c * CT);  // V: zeros behind the unit's tokens
         const int in_box = (1 << p.box_log2) - 1;
-        constexpr int kFlight = LR < 8 ? LR : 8;  // loads in flight, all before the first store
-#pragma unroll
-        for (int i0 = 0; i0 < LR; i0 += kFlight) {
+        constexpr int kFlight = LR < 8 ? 2 : 4;  // loads in flight, all before the first store
+#pragma unroll 1
+        for (int i0 = 0; i0 < LR / 2; i0 += kFlight) {
           uint4 code[kFlight];
 #pragma unroll
           for (int i = 0; i < kFlight; ++i) {
-            const int row = (i0 + i) * (64 / LR) + t / LR, x = t % LR;
+            const int row = (i0 + i) * (128 / LR) + t / LR, x = t % LR;
             code[i] = row < nv ? *reinterpret_cast<const uint4 *>(raw + (row >> p.box_log2) * p.box_pitch +
                                                                   (row & in_box) * D + x * 16)
                                : make_uint4(0, 0, 0, 0);
           }
 #pragma unroll
           for (int i = 0; i < kFlight; ++i) {
-            const int row = (i0 + i) * (64 / LR) + t / LR, x = t % LR;
+            const int row = (i0 + i) * (128 / LR) + t / LR, x = t % LR;
             uint4 a, b;  // codes 0-7 and 8-15
             e4m3x4_to_f16x2x2(code[i].x, a.x, a.y);
             e4m3x4_to_f16x2x2(code[i].y, a.z, a.w);
@@ -494,6 +497,8 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
     const uint32_t ocol = lanes + C::kOCol + w * D;
     float sl2 = fabsf(p.scale_log2);  // a negative scale's sign is in the score product
     uint32_t step = 0;               // steps of all units so far
+    uint32_t qphase = 0;             // E4M3: a bit per half of q
+    int half = 0;
     bool ok = true;
     SharedUnit u;
     for (int k = 0; ok && (ok = next_unit(k, u)) && u.chunks > 0; ++k) {
@@ -506,14 +511,18 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
       int nv = u.tok1 - u.tok0 - (two ? 0 : j0) * CT;         // tokens of the step's chunk and behind it
       float m = -INFINITY, l = 0.f;
       if constexpr (F8) {  // the power of two that the row's q was scaled by
-        const int bi = r / p.gt, head = r - bi * p.gt;
-        uint32_t top = 0;
-        if (r < u.rows && head < u.heads) {
-          const uint16_t *q = p.q + (u.b0 + bi) * p.q_sb + (int64_t)(u.kvh * p.g + u.ht * p.gt + head) * p.q_sh;
-#pragma unroll
-          for (int i = 0; i < D; i += 8) top = max_abs(top, __ldg(reinterpret_cast<const uint4 *>(q + i)));
+        const bool both = NACC == 2 && q_box_rows(u) > kTileRows;
+        const int h = both || NACC == 1 ? 0 : half;
+        if (!both && NACC == 2) half ^= 1;
+        ok = __all_sync(0xffffffffu, wait(q_full + 8 * h, qphase >> h & 1) && (!both || wait(q_full + 8, qphase >> 1)));
+        if (!ok) break;
+        qphase ^= both ? 3 : 1 << h;
+        sl2 = fabsf(p.scale_log2) * (r < u.rows ? unscale[h * kTileRows + r] : 1.f);
+        __syncwarp();
+        if (lane == 0) {
+          tc::arrive(q_empty + 8 * h);
+          if (both) tc::arrive(q_empty + 8);
         }
-        sl2 = fabsf(p.scale_log2) * pow2(-q_exponent(top));
       }
       const uint64_t scale = duo(sl2, sl2);
       for (int j = j0; ok && j < steps; j += NACC, nv -= (two ? 1 : NACC) * CT) {
@@ -523,23 +532,27 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
         if (live) {
           tc::fence_after();
           const uint32_t scol = lanes + buf * C::kSCol;
-          float s[CT];
-          tc::ld32(scol, s);
-          tc::ld32(scol + 32, s + 32);
-          tc::wait_ld();
-          if (nv < CT) {
-#pragma unroll
-            for (int i = 0; i < CT; ++i)
-              if (i >= nv) s[i] = -INFINITY;
-          }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+// Not unrolled, and the scores read twice: with a tile's 64 scores held, the roles of a
+// unit change did not fit the instruction cache beside one another.
+#pragma unroll 1
+          for (int i0 = 0; i0 < CT; i0 += 32) {
+            float s[32];
+            tc::ld32(scol + i0, s);
+            tc::wait_ld32(s);
+            if (nv < i0 + 32) {
 #pragma unroll
-          for (int i = 0; i < CT; i += 2) mx[i >> 1 & 3] = fmaxf(fmaxf(mx[i >> 1 & 3], s[i]), s[i + 1]);
+              for (int i = 0; i < 32; ++i)
+                if (i0 + i >= nv) s[i] = -INFINITY;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) mx[i >> 1 & 3] = fmaxf(fmaxf(mx[i >> 1 & 3], s[i]), s[i + 1]);
+          }
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
           // The reference moves only when a score passes it by 2^8: any
           // reference gives the same result as long as l and O share it, and the
           // rescale of O is skipped on almost every chunk.
-          if (__any_sync(0xffffffffu, top > m + 8.f)) {
+          if (__any_sync(0xffffffffu, r < u.rows && top > m + 8.f)) {
             const float mn = fmaxf(m, top);
             const float a = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
             m = mn;
@@ -563,12 +576,20 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
           const float ref = m == -INFINITY ? 0.f : m;
           const uint64_t shift = duo(-ref, -ref);
           uint64_t ls[2] = {0, 0};
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < CT; i += 32) {
+            float s[32];
+            tc::ld32(scol + i, s);
+            tc::wait_ld32(s);
+            if (nv < i + 32) {
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                if (i + x >= nv) s[x] = -INFINITY;
+            }
             uint32_t pk[16];
 #pragma unroll
             for (int x = 0; x < 32; x += 2) {
-              float2 e = parts(fma2(duo(s[i + x], s[i + x + 1]), scale, shift));
+              float2 e = parts(fma2(duo(s[x], s[x + 1]), scale, shift));
               e.x = fast_exp2(e.x);
               e.y = fast_exp2(e.y);
               ls[x >> 1 & 1] = add2(ls[x >> 1 & 1], duo(e.x, e.y));
@@ -592,11 +613,11 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
           const float inv = 1.f / l;
           const int64_t row = u.part + (two || NACC == 1 ? 0 : (int64_t)j0 * u.rows) + r;
           float4 *dst = reinterpret_cast<float4 *>(p.o_part + row * D);
-#pragma unroll
+#pragma unroll 1
           for (int i = 0; i < D; i += 32) {
             float o[32];
             tc::ld32(ocol + i, o);
-            tc::wait_ld();
+            tc::wait_ld32(o);
             if (r < u.rows) {
 #pragma unroll
               for (int x = 0; x < 8; ++x)

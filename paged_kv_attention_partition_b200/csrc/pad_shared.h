@@ -46,8 +46,6 @@ enum SharedBox : int32_t {
 struct SharedParams {
   CUtensorMap tmk, tmv;    // caches, boxes as box_kind says
   CUtensorMap tmqp, tmqr;  // q: boxes of 64 head_dim x gt heads x nseq sequences (prefix), x 1 (rest)
-  const uint16_t *q;
-  int64_t q_sb, q_sh;
   const int32_t *shared_table;
   const int32_t *tables;
   int64_t table_stride;

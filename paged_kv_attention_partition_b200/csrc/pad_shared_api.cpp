@@ -52,10 +52,10 @@ Layout layout(const Shape &s, int ctas, pad::SharedParams *p) {
   p->bs_log2 = 0;
   while ((1ll << p->bs_log2) < s.bs) ++p->bs_log2;
   // in hundreds of cycles, from the kernel's own clocks on B200 (D = 128)
-  p->w_item = s.fp8 ? 80 : 30;
+  p->w_item = s.fp8 ? 60 : 30;
   p->w_pre1 = s.fp8 ? 14 : 11;
   p->w_pre2 = s.fp8 ? 26 : 20;
-  p->w_rest = s.fp8 ? 18 : 11;
+  p->w_rest = s.fp8 ? 14 : 11;
   const int full = pad::shared_part_rows((int)(nseq * gt), (int)s.D);
   const int last = pad::shared_part_rows((int)((s.B - (p->nrb - 1) * nseq) * gt), (int)s.D);
   p->pre_rows = full > last ? full : last;
@@ -295,9 +295,6 @@ extern "C" pad_status pad_decode_shared(const pad_tensor *q, const pad_tensor *k
   if ((st = cache_map(&p.tmv, v_cache, p, "v_cache")) != PAD_OK) return st;
   if ((st = query_map(&p.tmqp, q, p.gt, p.nseq)) != PAD_OK) return st;
   if ((st = query_map(&p.tmqr, q, p.gt, 1)) != PAD_OK) return st;
-  p.q = static_cast<const uint16_t *>(q->data);
-  p.q_sb = q->stride[0];
-  p.q_sh = q->stride[1];
   p.shared_table = static_cast<const int32_t *>(shared_table->data);
   p.tables = static_cast<const int32_t *>(block_tables->data);
   p.table_stride = block_tables->stride[0];
