@@ -51,11 +51,16 @@ Layout layout(const Shape &s, int ctas, pad::SharedParams *p) {
   p->max_blocks = (int32_t)s.W;
   p->bs_log2 = 0;
   while ((1ll << p->bs_log2) < s.bs) ++p->bs_log2;
-  // in hundreds of cycles, from the kernel's own clocks on B200 (D = 128)
-  p->w_item = s.fp8 ? 60 : 30;
+  // In hundreds of cycles: begun with the kernel's own clocks on B200, then swept on
+  // seven bf16 and six E4M3 shapes (head_dim 64 to 256, 6 to 256 sequences).  bf16, 64
+  // sequences of 40 / 8 heads behind 8192 tokens and 256 of 32 / 8 behind 32768:
+  // 30 / 11 / 20 / 11 51.9 and 196 us, 40 / 11 / 20 / 9 49.8 and 196, 20 / 11 / 20 / 9
+  // 47.8 and 225.  E4M3, 48 sequences of 32 / 8 heads behind 6000 tokens: 80 / 14 / 26 / 18
+  // 46.7 us, 60 / 14 / 26 / 14 43.3.
+  p->w_item = s.fp8 ? 60 : 40;
   p->w_pre1 = s.fp8 ? 14 : 11;
   p->w_pre2 = s.fp8 ? 26 : 20;
-  p->w_rest = s.fp8 ? 14 : 11;
+  p->w_rest = s.fp8 ? 14 : 9;
   const int full = pad::shared_part_rows((int)(nseq * gt), (int)s.D);
   const int last = pad::shared_part_rows((int)((s.B - (p->nrb - 1) * nseq) * gt), (int)s.D);
   p->pre_rows = full > last ? full : last;
