@@ -14,6 +14,7 @@
 #include <map>
 #include <set>
 #include <mutex>
+#include <new>
 #include <string>
 #include <utility>
 #include <vector>
@@ -602,7 +603,14 @@ pad_status host_scratch(int device, cudaStream_t stream, size_t bytes, void **ou
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
   const bool capturing = cs != cudaStreamCaptureStatusNone;
   std::lock_guard<std::mutex> lock(g_ws_mu);
-  Scratch &s = g_scratch[{device, stream}];
+  Scratch *entry = nullptr;
+  try {
+    entry = &g_scratch[{device, stream}];
+    g_scratch_kept.reserve(g_scratch_kept.size() + 1);
+  } catch (const std::bad_alloc &) {
+    return fail(PAD_ERR_WORKSPACE, "out of host memory");
+  }
+  Scratch &s = *entry;
   if (s.ws.bytes < bytes) {
     if (capturing)
       return fail(PAD_ERR_WORKSPACE,
@@ -856,13 +864,19 @@ pad_status pad_release_workspace(int32_t device) {
       it = pool->erase(it);
     }
   }
-  std::vector<std::pair<int, void *>> drop;
+  auto drop = [&](int d, void *ptr) -> cudaError_t {
+    if ((e = cudaSetDevice(d)) != cudaSuccess) return e;
+    if ((e = cudaDeviceSynchronize()) != cudaSuccess) return e;
+    cudaFree(ptr);
+    return cudaSuccess;
+  };
   for (auto it = g_scratch.begin(); it != g_scratch.end();) {
     if (device >= 0 && it->first.first != device) {
       ++it;
       continue;
     }
-    if (it->second.ws.ptr != nullptr) drop.push_back({it->first.first, it->second.ws.ptr});
+    if (it->second.ws.ptr != nullptr && drop(it->first.first, it->second.ws.ptr) != cudaSuccess)
+      return cuda_fail(e, "releasing scratch");
     it = g_scratch.erase(it);
   }
   for (size_t i = 0; i < g_scratch_kept.size();) {
@@ -870,13 +884,9 @@ pad_status pad_release_workspace(int32_t device) {
       ++i;
       continue;
     }
-    drop.push_back(g_scratch_kept[i]);
+    if (drop(g_scratch_kept[i].first, g_scratch_kept[i].second) != cudaSuccess)
+      return cuda_fail(e, "releasing scratch");
     g_scratch_kept.erase(g_scratch_kept.begin() + (long)i);
-  }
-  for (const auto &d : drop) {
-    if ((e = cudaSetDevice(d.first)) != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
-    if ((e = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
-    cudaFree(d.second);
   }
   if ((e = cudaSetDevice(cur)) != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
   return PAD_OK;

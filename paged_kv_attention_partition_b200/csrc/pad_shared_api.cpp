@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include <mutex>
+
 #include "pad.h"
 #include "pad_host.h"
 #include "pad_internal.h"
@@ -163,8 +165,11 @@ pad_status query_map(CUtensorMap *map, const pad_tensor *q, int heads, int seqs)
   return PAD_OK;
 }
 
+// The current device, its context made current too: in a thread that has made no
+// CUDA call of its own yet the tensor-map encoder, a driver call, would find none.
 pad_status current_device(int *device) {
-  const cudaError_t e = cudaGetDevice(device);
+  cudaError_t e = cudaGetDevice(device);
+  if (e == cudaSuccess) e = cudaSetDevice(*device);
   return e == cudaSuccess ? PAD_OK : pad::host_cuda_fail(e, "cudaGetDevice");
 }
 
@@ -292,8 +297,6 @@ extern "C" pad_status pad_decode_shared(const pad_tensor *q, const pad_tensor *k
     if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
       return host_fail(PAD_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
     if ((st = pad::host_check_device_ptr(workspace, device, "workspace")) != PAD_OK) return st;
-  } else if ((st = pad::host_scratch(device, stream, l.total, &workspace)) != PAD_OK) {
-    return st;
   }
   choose_box(k_cache, v_cache, pad::kSharedChunk, &p);
   if ((st = cache_map(&p.tmk, k_cache, p, "k_cache")) != PAD_OK) return st;
@@ -317,11 +320,16 @@ extern "C" pad_status pad_decode_shared(const pad_tensor *q, const pad_tensor *k
   p.lse = lse != nullptr ? static_cast<float *>(lse->data) : nullptr;
   p.lse_sb = lse != nullptr ? lse->stride[0] : 0;
   p.lse_sh = lse != nullptr ? lse->stride[1] : 0;
+  cudaError_t e = pad::device_error_word(device, &p.err);
+  if (e != cudaSuccess) return pad::host_cuda_fail(e, "error word");
+  // Two threads on one stream share its scratch: neither's kernels between the
+  // other's two, nor a larger buffer between the other's look and its launches.
+  static std::mutex launches;
+  std::lock_guard<std::mutex> lock(launches);
+  if (workspace == nullptr && (st = pad::host_scratch(device, stream, l.total, &workspace)) != PAD_OK) return st;
   char *base = static_cast<char *>(workspace);
   p.o_part = reinterpret_cast<float *>(base + l.o_part);
   p.lse_part = reinterpret_cast<float *>(base + l.lse_part);
-  cudaError_t e = pad::device_error_word(device, &p.err);
-  if (e != cudaSuccess) return pad::host_cuda_fail(e, "error word");
   e = pad::launch_shared(p, (int)D, fp8, stream);
   return e == cudaSuccess ? PAD_OK : pad::host_cuda_fail(e, "shared-prefix decode launch");
 }

@@ -261,6 +261,66 @@ def test_two_streams_at_once(cuda_device):
             check(out, lse, ref, "two streams")
 
 
+def test_two_threads_on_one_stream(cuda_device):
+    # one scratch: the threads' kernels must not come between one another's
+    import threading
+    batches = [Batch(B, 8, 2, 128, 16, 30, [5 * i for i in range(B)], seed=s) for B, s in ((4, 22), (30, 23))]
+    args = [b.device(cuda_device) for b in batches]
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        for _ in range(30):
+            got[i].append(pad.pad_decode_shared(**args[i], lse=True, stream=stream))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    for b, results in zip(batches, got):
+        assert len(results) == 30
+        ref = b.reference()
+        for out, lse in results:
+            check(out, lse, ref, "two threads")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_non_finite_query_rows_stay_alone(cuda_device, kv):
+    batch = Batch(20, 8, 2, 128, 16, 12, [9 * i for i in range(20)], kv=kv, seed=24)
+    ref = batch.reference()
+    bad = torch.zeros(20, 8, dtype=torch.bool)
+    for b, h, x in ((0, 0, float("nan")), (7, 5, float("inf")), (19, 7, -float("inf"))):
+        batch.q[b, h, 3] = x
+        bad[b, h] = True
+    out, lse = run(batch, cuda_device)
+    assert bool(out.isnan().any(-1).cpu()[bad].all())
+    ref[0][bad] = 0.0
+    out[bad.to(cuda_device)] = 0
+    lse = torch.where(bad.to(cuda_device), ref[1].float().to(cuda_device), lse)
+    check(out, lse, ref, "other rows")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("power", [-90, 90])
+def test_query_rows_far_from_one(cuda_device, kv, power):
+    # rows of 2^power under a scale of 2^-power, some of zeros
+    batch = Batch(6, 8, 2, 128, 16, 9, [0, 1, 63, 64, 65, 200], kv=kv, seed=25)
+    batch.q = (batch.q.float() * 2.0 ** power).to(torch.bfloat16)
+    batch.q[2, 3] = 0
+    batch.scale *= 2.0 ** -power
+    out, lse = run(batch, cuda_device)
+    check(out, lse, batch.reference(), str(power))
+
+
+def test_thousands_of_sequences(cuda_device):
+    # many rounds of the schedule's sums, a row block of every kind, one-token items
+    B = 2100
+    batch = Batch(B, 2, 1, 64, 8, 3, [(7 * i) % 11 for i in range(B)], seed=26, empty=tuple(range(3, B, 17)))
+    out, lse = run(batch, cuda_device)
+    check(out, lse, batch.reference(), "thousands")
+
+
 def test_strided_out_and_lse(cuda_device):
     batch = Batch(4, 8, 2, 128, 16, 10, [0, 3, 200, 7], seed=20)
     a = batch.device(cuda_device)
