@@ -10,8 +10,8 @@
 // the second; neighbours: any), so the rotation needs no exchange between lanes
 // and the norm one reduction over D / 16 lanes.  A warp keeps one token: its angles are
 // computed once, and weight times cosine and sine once per tensor, which leaves per
-// element a product, a multiply-add and the row's scale, two elements at a time:
-//   y1 = inv (x1 (w1 cos) + x2 (-w2 sin)),  y2 = inv (x2 (w2 cos) + x1 (w1 sin)).
+// element the row's scale, a product and a multiply-add, two elements at a time:
+//   y1 = (inv x1) (w1 cos) + (inv x2) (-w2 sin),  y2 = (inv x2) (w2 cos) + (inv x1) (w1 sin).
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -255,20 +255,24 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 5) rows_kernel(const __grid_c
         inv = rsqrtf(s * (1.f / D) + p.eps);
       }
       if (rows_left <= 0) continue;
-      const uint64_t inv2 = duo(inv, inv);
+      if (weights != nullptr) {  // first: a weight's product with a row that is still large may not be one
+        const uint64_t inv2 = duo(inv, inv);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a.p[i] = mul2(a.p[i], inv2), b.p[i] = mul2(b.p[i], inv2);
+      }
       if (spin) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint64_t x = fma2(INTERLEAVED ? swapped(a.p[i]) : b.p[i], ua.p[i], mul2(a.p[i], wa.p[i]));
           const uint64_t y = fma2(INTERLEAVED ? swapped(b.p[i]) : a.p[i], ub.p[i], mul2(b.p[i], wb.p[i]));
-          a.p[i] = mul2(x, inv2);
-          b.p[i] = mul2(y, inv2);
+          a.p[i] = x;
+          b.p[i] = y;
         }
       } else if (weights != nullptr) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          a.p[i] = mul2(mul2(a.p[i], wa.p[i]), inv2);
-          b.p[i] = mul2(mul2(b.p[i], wb.p[i]), inv2);
+          a.p[i] = mul2(a.p[i], wa.p[i]);
+          b.p[i] = mul2(b.p[i], wb.p[i]);
         }
       }
       if (kCodes && codes) {

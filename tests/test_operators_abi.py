@@ -128,6 +128,10 @@ def call_append(lib, eps=1e-6, ks=0.0, vs=0.0, **over):
     (dict(vs=-1.0), pad.PAD_ERR_INVALID_ARG),
     (dict(kc=(F8, (12, 2, 16, 128)), vc=(F8, (12, 2, 16, 128)), ks=float("inf")), pad.PAD_ERR_INVALID_ARG),
     (dict(eps=float("inf")), pad.PAD_ERR_INVALID_ARG),
+    (dict(kc=(F8, (12, 2, 16, 128)), vc=(F8, (12, 2, 16, 128)), ks=2.0 ** -101), pad.PAD_ERR_UNSUPPORTED),
+    (dict(kc=(F8, (12, 2, 16, 128)), vc=(F8, (12, 2, 16, 128)), vs=2.0 ** 101), pad.PAD_ERR_UNSUPPORTED),
+    (dict(kw=(BF, (128,), None, 0x100008)), pad.PAD_ERR_INVALID_ARG),         # a weight off its 16 bytes
+    (dict(qw=(F32, (128,), None, 0x100004)), pad.PAD_ERR_INVALID_ARG),
 ])
 def test_append_refusals(lib, over, status):
     refused(call_append(lib, **over), status)

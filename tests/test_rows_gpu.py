@@ -197,6 +197,37 @@ def test_append_e4m3_edges(cuda_device):
             assert torch.equal(torch.signbit(got)[num], torch.signbit(want.view(-1).float())[num])
 
 
+@pytest.mark.parametrize("scale", [1.0, 0.03125, 3.0 / 64, 0.7, 1e-3, 2.0 ** -100, 2.0 ** 100])
+def test_append_e4m3_codes_of_every_bf16(cuda_device, scale):
+    # the fp32 quotient rounded once, code for code
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16)
+    k = bits.view(torch.bfloat16).view(64, 8, 128)
+    kc = torch.zeros(4, 8, 16, 128, dtype=torch.float8_e4m3fn, device=cuda_device)
+    vc = torch.zeros_like(kc)
+    pos = torch.arange(64, dtype=torch.int32, device=cuda_device)
+    tables = torch.arange(4, dtype=torch.int32, device=cuda_device).view(1, 4)
+    d = k.to(cuda_device)
+    pad.pad_append_kv(d, d, pos, tables, kc, vc, seq_ids=torch.zeros_like(pos), k_scale=scale, v_scale=scale)
+    s = torch.tensor(scale, dtype=torch.float32)
+    want = (k.float() / s).clamp(-448, 448).to(torch.float8_e4m3fn).transpose(0, 1).reshape(8, 4, 16, 128).transpose(0, 1)
+    num = ~want.float().isnan()
+    for c in (kc.cpu(), vc.cpu()):
+        assert torch.equal(c.float().isnan(), ~num)
+        assert torch.equal(c.view(torch.uint8)[num], want.contiguous().view(torch.uint8)[num])
+
+
+def test_norm_rope_of_the_largest_values(cuda_device):
+    # the sum of squares passes fp32's range: rows of zeros, as rsqrt(inf) gives, not NaN
+    q = torch.full((3, 4, 128), 3e38, dtype=torch.bfloat16, device=cuda_device)
+    q[1] *= -1
+    w = torch.full((128,), 8.0, device=cuda_device)
+    pos = torch.tensor([0, 5, 1 << 30], dtype=torch.int32, device=cuda_device)
+    f = torch.rand(64, generator=torch.Generator().manual_seed(0)).to(cuda_device)
+    for inter in (False, True):
+        out, _ = pad.pad_qk_norm_rope(q, None, w, None, pos, f, interleaved=inter)
+        assert bool((out == 0).all())
+
+
 def test_append_refuses_bad_places_token_by_token(cuda_device):
     # a position outside the table, a sequence that is not there, a block that is
     # not there: flagged and not written; every other token is
