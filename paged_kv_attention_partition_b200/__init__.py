@@ -340,17 +340,8 @@ def _load_fast():
     return module
 
 
-def _invoke(fn, first: torch.Tensor, stream, *args):
-    """``fn(*args, stream)`` on the device of ``first``; its outputs, or PadError."""
-    dev = first.device
-    if dev.type != "cuda":
-        raise ValueError(f"expected CUDA tensors, got one on {dev}")
-    handle = torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream_handle(stream, dev)
-    if dev.index == torch.cuda.current_device():
-        r = fn(*args, handle)
-    else:
-        with torch.cuda.device(dev):
-            r = fn(*args, handle)
+def _checked(r):
+    """A _pad_torch call's outputs; PadError for a status."""
     if type(r) is int:
         _raise(r)
     return r
@@ -367,8 +358,9 @@ def pad_qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor], q_weight: Optio
     Without a weight that tensor is not normed; without ``inv_freq`` (fp32 [R/2],
     with ``positions`` int32 [T]) nothing is rotated; k may be None.  ``q_out`` /
     ``k_out`` receive the rows (they may be q and k themselves).  Returns (q_out, k_out)."""
-    return _invoke((_fast or _load_fast()).qk_norm_rope, q, stream, q, k, q_weight, k_weight, positions, inv_freq, eps,
-                   interleaved, q_out, k_out)
+    return _checked((_fast or _load_fast()).qk_norm_rope(
+        q, k, q_weight, k_weight, positions, inv_freq, eps, interleaved, q_out, k_out,
+        None if stream is None else _stream_handle(stream, None)))
 
 
 def pad_append_kv(k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, block_tables: torch.Tensor,
@@ -385,8 +377,9 @@ def pad_append_kv(k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor, blo
     sequence t's).  ``q`` [T, Hq, D]: the tokens' query rows, normed and rotated by
     the same launch into ``q_out``.  An E4M3 cache holds x / ``k_scale``, x /
     ``v_scale``.  Returns q_out (None without q)."""
-    return _invoke((_fast or _load_fast()).append_kv, k, stream, k, v, positions, block_tables, k_cache, v_cache,
-                   seq_ids, inv_freq, interleaved, k_weight, eps, q, q_weight, q_out, k_scale, v_scale)
+    return _checked((_fast or _load_fast()).append_kv(
+        k, v, positions, block_tables, k_cache, v_cache, seq_ids, inv_freq, interleaved, k_weight, eps, q, q_weight,
+        q_out, k_scale, v_scale, None if stream is None else _stream_handle(stream, None)))
 
 
 def pad_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, shared_table: torch.Tensor,
@@ -400,8 +393,9 @@ def pad_decode_shared(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     least n * block_size.  ``workspace``: a contiguous tensor of at least
     ``pad_decode_shared_plan(...)["workspace_bytes"]`` bytes instead of the
     library's scratch.  Returns (out, lse)."""
-    return _invoke((_fast or _load_fast()).decode_shared, q, stream, q, k_cache, v_cache, shared_table, block_tables,
-                   seq_lens, scale, out, lse, sinks, k_scale, v_scale, workspace)
+    return _checked((_fast or _load_fast()).decode_shared(
+        q, k_cache, v_cache, shared_table, block_tables, seq_lens, scale, out, lse, sinks, k_scale, v_scale, workspace,
+        None if stream is None else _stream_handle(stream, None)))
 
 
 def pad_decode_shared_plan(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, block_size: int,

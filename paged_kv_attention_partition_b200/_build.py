@@ -53,10 +53,10 @@ def binding_command(out: str):
 
     root = os.path.dirname(torch.__file__)
     inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
-           sysconfig.get_paths()["include"], INCLUDE]
+           sysconfig.get_paths()["include"], INCLUDE, os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
             *(f"-I{d}" for d in inc), os.path.join(CSRC, "pad_torch.cpp"), "-o", out, f"-L{os.path.join(root, 'lib')}",
-            "-ltorch_python", "-ltorch_cpu", "-lc10"]
+            "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
 
 
 def build_binding(force: bool = False) -> str:
