@@ -643,18 +643,28 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
   }
 }
 
-// One warp per query row: the row's prefix units and rest units, found again
+// One to four warps per query row: the row's prefix units and rest units, found again
 // from the lengths, weighted by their log-sum-exp.  What needs only the lengths is
 // done before the partial kernel has ended.
 constexpr int kMergeWarps = 8;
-template <int D>
+__host__ __device__ __forceinline__ int merge_ctas(int Hq, int wpr) { return (Hq * wpr + kMergeWarps - 1) / kMergeWarps; }
+// Sum over a warp of values in [0, 2^58): two halves' worth of bits at a time, which
+// one instruction adds up without a carry out of 32.
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+  int64_t sum = (int64_t)__reduce_add_sync(0xffffffffu, (uint32_t)v & 0x3ffffffu) +
+                ((int64_t)__reduce_add_sync(0xffffffffu, (uint32_t)(v >> 26) & 0x3ffffffu) << 26);
+  if (__any_sync(0xffffffffu, v >> 52 != 0)) sum += (int64_t)__reduce_add_sync(0xffffffffu, (uint32_t)(v >> 52)) << 52;
+  return sum;
+}
+template <int D, int VEC>
 __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __grid_constant__ SharedParams p) {
-  constexpr int VEC = D / 32;
+  constexpr int WPR = D / (32 * VEC);  // warps of a row
   constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.4426950408889634f;
   __shared__ int64_t sums[2][kMergeWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per_seq = (p.Hq + kMergeWarps - 1) / kMergeWarps;
-  const int b = (int)(blockIdx.x / per_seq), h = (int)(blockIdx.x % per_seq) * kMergeWarps + warp;
+  const int per_seq = merge_ctas(p.Hq, WPR);
+  const int b = (int)(blockIdx.x / per_seq), wh = (int)(blockIdx.x % per_seq) * kMergeWarps + warp;
+  const int h = wh / WPR, col = (wh % WPR * 32 + lane) * VEC;
   // costs of all rest items, and of those of the sequences before b
   int64_t all = 0, before = 0;
   bool bad;
@@ -663,11 +673,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
     all += c;
     if (x < b) before += c;
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    all += __shfl_xor_sync(0xffffffffu, all, off);
-    before += __shfl_xor_sync(0xffffffffu, before, off);
-  }
+  all = warp_sum(all);
+  before = warp_sum(before);
   if (lane == 0) {
     sums[0][warp] = all;
     sums[1][warp] = before;
@@ -726,7 +733,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
   for (int i0 = 0; i0 < pi.n + ri.n; i0 += 32) {  // lane: one candidate
     const int i = i0 + lane;
     float s = -INFINITY;
-    int64_t r = 0;
+    uint32_t r = 0;  // (2^32 part rows would be a workspace of a terabyte)
     if (i < pi.n + ri.n) {
       const Item &it = i < pi.n ? pi : ri;
       const int x = i < pi.n ? i : i - pi.n;
@@ -735,7 +742,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
       const int n = shared_cut(p, (c + 1) * q - it.start, it.w, it.chunks) -
                     shared_cut(p, c * q - it.start, it.w, it.chunks);
       if (a < n) {
-        r = it.part + c * it.stride + a * it.rows;
+        r = (uint32_t)(it.part + c * it.stride + a * it.rows);
         s = p.lse_part[r];
       }
     }
@@ -752,21 +759,25 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
 #pragma unroll
     for (int x = 0; x < VEC; ++x) acc[x] *= a;
     uint32_t todo = __ballot_sync(0xffffffffu, s != -INFINITY);
-    constexpr int kFlight = 32 / VEC < 8 ? 32 / VEC : 8;
+    constexpr int kFlight = 32 / VEC;
     while (todo != 0) {  // several partials in flight
       float o[kFlight][VEC], wj[kFlight];
 #pragma unroll
       for (int y = 0; y < kFlight; ++y) {
         const int jl = todo != 0 ? __ffs(todo) - 1 : 0;
-        const int64_t rj = __shfl_sync(0xffffffffu, r, jl);
+        const uint32_t rj = __shfl_sync(0xffffffffu, r, jl);
         wj[y] = todo != 0 ? __shfl_sync(0xffffffffu, w, jl) : 0.f;
         if (todo != 0) {
-          const float *src = p.o_part + rj * D + lane * VEC;
+          const float *src = p.o_part + (int64_t)rj * D + col;
+          if constexpr (VEC == 2) {
+            const float2 f = *reinterpret_cast<const float2 *>(src);
+            o[y][0] = f.x, o[y][1] = f.y;
+          } else {
 #pragma unroll
-          for (int x = 0; x < VEC; x += 2) {
-            const float2 f = *reinterpret_cast<const float2 *>(src + x);
-            o[y][x] = f.x;
-            o[y][x + 1] = f.y;
+            for (int x = 0; x < VEC; x += 4) {
+              const float4 f = *reinterpret_cast<const float4 *>(src + x);
+              o[y][x] = f.x, o[y][x + 1] = f.y, o[y][x + 2] = f.z, o[y][x + 3] = f.w;
+            }
           }
         } else {
 #pragma unroll
@@ -789,11 +800,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
   }
   if (m == -INFINITY && p.sinks == nullptr) lse2 = -INFINITY;
   const float w = m == -INFINITY ? 0.f : exp2f(m - lse2) * p.v_scale;
-  uint16_t *o = p.out + b * p.o_sb + (int64_t)h * p.o_sh + lane * VEC;
+  uint16_t *o = p.out + b * p.o_sb + (int64_t)h * p.o_sh + col;
 #pragma unroll
   for (int i = 0; i < VEC; i += 2)
     *reinterpret_cast<uint32_t *>(o + i) = pack_bf16x2(acc[i] * w, acc[i + 1] * w);
-  if (lane == 0 && p.lse != nullptr) p.lse[b * p.lse_sb + (int64_t)h * p.lse_sh] = lse2 * kLn2;
+  if (col == 0 && p.lse != nullptr) p.lse[b * p.lse_sb + (int64_t)h * p.lse_sh] = lse2 * kLn2;
 }
 
 template <int D, bool F8>
@@ -816,12 +827,20 @@ cudaError_t launch_t(const SharedParams &p, cudaStream_t s) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)p.B * (unsigned)((p.Hq + kMergeWarps - 1) / kMergeWarps));
+  // Two elements a lane, so more warps for a row, each with more of its partials in
+  // flight, while all the warps fit the SMs at once; four beyond.  Two against four: 24
+  // sequences of 16 heads of 256 31.7 / 32.5 us in all, 48 of 32 of 128 43.1 / 44.2;
+  // 64 of 40 of 128 52.6 / 49.7, 131 of 32 40.5 / 37.8.
+  constexpr int kWide = D == 64 ? 2 : 4, kFine = 2;
+  const int64_t fine_warps = (int64_t)p.B * p.Hq * (D / (32 * kFine));
+  const bool fine = fine_warps <= (int64_t)p.ctas * 24;
+  cfg.gridDim = dim3((unsigned)p.B * (unsigned)merge_ctas(p.Hq, D / (32 * (fine ? kFine : kWide))));
   cfg.blockDim = dim3(kMergeWarps * 32);
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, shared_merge_kernel<D>, p);
+  return fine ? cudaLaunchKernelEx(&cfg, shared_merge_kernel<D, kFine>, p)
+              : cudaLaunchKernelEx(&cfg, shared_merge_kernel<D, kWide>, p);
 }
 
 }  // namespace
