@@ -33,7 +33,7 @@ namespace {
 //   softmax warps   thread = row: scores out of tensor memory, running maximum and
 //                   sum, P back over the scores
 //   widening warps  (E4M3 cache) the copies' codes, from a small ring of their own, to
-//                   f16 operands: two warps for q and K, two for V
+//                   f16 operands: four warps for K, four for V, q's rows by all
 //
 // Every E4M3 code is an f16 value, and q is scaled per row by a power of two that
 // puts its largest element into [2^14, 2^15), where its bf16 values are f16 values
@@ -47,13 +47,30 @@ namespace {
 // At D = 256 there is one accumulator (256 of the 512 columns) and one softmax group.
 //
 // The P of a step overlays its S, so QK(n + NBUF) waits for PV(n).  Four buffers of 64
-// tokens keep the next scores ready when a group has written P.  Measured on B200,
-// 256 sequences of 32 / 8 heads of 128 behind 32768 shared tokens: 153 us; two
-// buffers of 128 tokens with two threads per row 161 us (rows of 128 scores do not fit
-// one thread's registers); a quarter of the exponentials on the FMA pipe instead
-// of ex2 154 us, half 163 us.  The products are issued by two warps because between
-// two of them a warp spends about as long on its waits and counters as the tensor
-// core on a product: from one warp the products' issue was half of its time.
+// tokens keep the next scores ready when a group has written P.  The products are
+// issued by two warps because between two of them a warp spends about as long on its
+// waits and counters as the tensor core on a product: from one warp the products' issue
+// was half of its time.
+//
+// Rounding: P to 16 bits (bf16; f16 with an E4M3 cache), the operand's type; l sums the
+// weights before that, in fp32, as O and the partials are.
+//
+// Measured on B200 (bf16 unless said; merge included):
+//   256 sequences of 32 / 8 heads of 128 behind 32768 tokens: 142 us, 970 TFLOP/s, 58 %
+//     of the measured matrix peak; 64 of 40 / 8, 8192 tokens of their own each: 335 us,
+//     6.4 TB/s, 98 % of the measured copy rate.  The first is bound by the chain scores ->
+//     exponentials -> product of two tiles taking turns (tensor pipe 30 to 60 % busy, the
+//     exponentials' pipe about half), the second by HBM.
+//   Two buffers of 128 tokens with two threads per row 161 us where this kernel, then,
+//     took 153; a quarter of the exponentials on the FMA pipe instead of ex2 154, half
+//     163; a pair of issuing warps per accumulator the same within 1 %.
+//   Rest items (a few rows, a few chunks) are bound by latency and by instruction
+//     fetches: a unit change runs every role's code, and warps then wait for instructions
+//     longer than for anything but data.  Scores read from tensor memory twice, a half at
+//     a time in loops that are not unrolled, instead of once into 64 registers: 256
+//     sequences with up to 400 tokens behind those 32768 206 -> 195 us.
+//   E4M3, 48 sequences of 32 / 8 heads behind 6000 tokens: 43 us, of which q's conversion
+//     with a thread per row took 10 and two widening warps per ring instead of four 2.
 template <int D, bool F8>
 struct SharedCfg {
   static constexpr int CT = kSharedChunk, NBUF = 4, NACC = shared_accs(D), CB = D / 64;
