@@ -136,6 +136,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, 5) rows_kernel(const __grid_c
   constexpr bool kCache = MODE != kRowsOut, kCodes = MODE == kRowsCacheE4m3;
   constexpr int kHeld = kCodes ? 1 : 2;  // bytes of a cached element
   __shared__ float2 turns[kRowsWarps][D / 2];  // cos, sin of the warp's token
+  // started beside the kernel before this one; nothing of that is read ahead of the wait
+  asm volatile("griddepcontrol.wait;\n griddepcontrol.launch_dependents;\n" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LPR, sub = lane / LPR;
   const int nq = (p.Hq + RPW - 1) / RPW, nk = (p.Hkv + RPW - 1) / RPW, steps = nq + nk * (kCache ? 2 : 1);
   const int share = (steps + p.steps_per_warp - 1) / p.steps_per_warp;
@@ -336,9 +338,16 @@ cudaError_t launch_t(RowsParams p, int sms, cudaStream_t s) {
   const int64_t warps = p.T * ((steps + p.steps_per_warp - 1) / p.steps_per_warp);
   const int64_t grid = (warps + kRowsWarps - 1) / kRowsWarps;
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-  if (p.interleaved) rows_kernel<D, MODE, true><<<(unsigned)grid, kRowsWarps * 32, 0, s>>>(p);
-  else rows_kernel<D, MODE, false><<<(unsigned)grid, kRowsWarps * 32, 0, s>>>(p);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kRowsWarps * 32);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, p.interleaved ? rows_kernel<D, MODE, true> : rows_kernel<D, MODE, false>, p);
 }
 
 template <int D>

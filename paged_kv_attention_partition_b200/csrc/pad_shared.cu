@@ -176,7 +176,9 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, words[0], 0);
-  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // the merge may come up as CTAs end
+  // What is above may run beside the kernel before this one; nothing below does.  The
+  // merge may come up from here on: it reads the lengths, which that kernel may write.
+  asm volatile("griddepcontrol.wait;\n griddepcontrol.launch_dependents;\n" ::: "memory");
 
   auto wait = [&](uint32_t bar, uint32_t parity, bool drain = false) {
     return tc::wait(bar, parity, p.err, abort_flag, drain);
@@ -697,7 +699,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
     sums[1][warp] = before;
   }
   __syncthreads();
-  if (h >= p.Hq) return;
+  if (h >= p.Hq) return;  // (counts as having let the next kernel start)
   all = before = 0;
 #pragma unroll
   for (int i = 0; i < kMergeWarps; ++i) {
@@ -747,6 +749,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
 #pragma unroll
   for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the partials are written
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // the next kernel's start may be beside what is left
   for (int i0 = 0; i0 < pi.n + ri.n; i0 += 32) {  // lane: one candidate
     const int i = i0 + lane;
     float s = -INFINITY;
@@ -837,13 +840,19 @@ cudaError_t launch_t(const SharedParams &p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     attr_done.fetch_or(bit, std::memory_order_acq_rel);
   }
-  shared_kernel<D, F8><<<p.ctas, C::kThreads, C::total, s>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  // comes up while the partial kernel's last CTAs run; waits for them before its first read
+  // Both come up beside the kernel before them, and wait for it before their first use
+  // of memory that it may write.
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)p.ctas);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::total;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, shared_kernel<D, F8>, p)) != cudaSuccess) return e;
   // Two elements a lane, so more warps for a row, each with more of its partials in
   // flight, while all the warps fit the SMs at once; four beyond.  Two against four: 24
   // sequences of 16 heads of 256 31.7 / 32.5 us in all, 48 of 32 of 128 43.1 / 44.2;
@@ -853,9 +862,7 @@ cudaError_t launch_t(const SharedParams &p, cudaStream_t s) {
   const bool fine = fine_warps <= (int64_t)p.ctas * 24;
   cfg.gridDim = dim3((unsigned)p.B * (unsigned)merge_ctas(p.Hq, D / (32 * (fine ? kFine : kWide))));
   cfg.blockDim = dim3(kMergeWarps * 32);
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.dynamicSmemBytes = 0;
   return fine ? cudaLaunchKernelEx(&cfg, shared_merge_kernel<D, kFine>, p)
               : cudaLaunchKernelEx(&cfg, shared_merge_kernel<D, kWide>, p);
 }

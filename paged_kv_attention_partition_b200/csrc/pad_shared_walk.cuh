@@ -124,12 +124,12 @@ __device__ __forceinline__ void shared_walk(const SharedParams &p, int cta, Emit
     pos = start + (rb == p.nrb - 1 ? pre.last : pre.full);
   }
 
-  int64_t base = pre.total;  // cost before this round's 32 sequences
+  int64_t base = pre.total;  // cost before these 32 sequences
   bool bad;
   int next = length(lane, &bad);
   for (int b0 = 0; b0 < p.B && pos < end; b0 += 32) {
     const int L = next;
-    next = length(b0 + 32 + lane, &bad);  // in flight during this round
+    next = length(b0 + 32 + lane, &bad);  // in flight meanwhile
     const int64_t item = shared_rest_cost(p, L);
     int64_t incl = item * hh;
 #pragma unroll

@@ -364,3 +364,61 @@ def test_a_serving_step(cuda_device):
         assert (out.double() - o2.double()).abs().max() <= 2 * 2.0 ** -8 * (vc.abs().max() + o2.abs().max()).double()
         assert (lse - l2).abs().max() <= 1e-4
     assert pad.pad_check_device_errors() == 0
+
+
+def test_a_captured_step_that_moves_its_lengths(cuda_device):
+    # lengths, inputs and cache written by the kernels and copies just before: each call
+    # starts beside its predecessor and must not read ahead of it
+    gen = torch.Generator().manual_seed(27)
+    B, Hq, Hkv, D, bs, n, W, steps = 6, 16, 4, 128, 16, 5, 9, 40
+    blocks = torch.randperm(n + B * (W - n), generator=gen).to(torch.int32)
+    tables = torch.cat([blocks[:n].expand(B, n), blocks[n:].view(B, W - n)], 1).contiguous().to(cuda_device)
+    cache = rand(gen, 2, len(blocks), Hkv, bs, D).to(torch.bfloat16).to(cuda_device)
+    f = torch.rand(D // 2, generator=gen).to(cuda_device)
+    host = torch.stack([rand(gen, B, Hq + 2 * Hkv, D) for _ in range(steps)]).to(torch.bfloat16)
+    rows = host.to(cuda_device)
+    at = torch.zeros(1, dtype=torch.int64, device=cuda_device)
+    lens = torch.full((B,), n * bs, dtype=torch.int32, device=cuda_device)
+    x = torch.zeros(B, Hq + 2 * Hkv, D, dtype=torch.bfloat16, device=cuda_device)
+    outs = torch.zeros(steps, B, Hq, D, dtype=torch.bfloat16, device=cuda_device)
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            x.copy_(rows.index_select(0, at)[0])
+        main.wait_stream(side)
+        q = pad.pad_append_kv(x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], lens, tables, cache[0], cache[1], inv_freq=f,
+                              q=x[:, :Hq])
+        lens.add_(1)
+        out, _ = pad.pad_decode_shared(q, cache[0], cache[1], tables[0, :n], tables, lens, D ** -0.5)
+        outs.index_copy_(0, at, out[None])
+        at.add_(1)
+
+    start = (cache.clone(), lens.clone())
+    for _ in range(steps):
+        step()
+    torch.cuda.synchronize()
+    want, held = outs.clone(), cache.clone()
+    cache.copy_(start[0])
+    lens.copy_(start[1])
+    at.zero_()
+    outs.zero_()
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(stream):
+        pad.pad_decode_shared(x[:, :Hq], cache[0], cache[1], tables[0, :n], tables, lens, D ** -0.5)  # its scratch
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        step()
+    for _ in range(steps):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(cache, held) and torch.equal(outs, want)
+    q = pad.pad_qk_norm_rope(rows[-1][:, :Hq], None, None, None, lens - 1, f)[0]
+    ref, _ = pad.pad_decode(q, cache[0], cache[1], tables, lens, D ** -0.5)
+    # both calls round each weight to bf16 once (2^-8 of sum w |v| <= max |v|) and out once
+    assert (outs[-1].double() - ref.double()).abs().max() <= 2 * 2.0 ** -8 * (cache[1].abs().max() + ref.abs().max()).double()
+    assert pad.pad_check_device_errors() == 0
