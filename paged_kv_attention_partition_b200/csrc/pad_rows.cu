@@ -14,10 +14,10 @@
 //   y1 = (inv x1) (w1 cos) + (inv x2) (-w2 sin),  y2 = (inv x2) (w2 cos) + (inv x1) (w1 sin).
 //
 // Measured on B200, beside the 6.56 TB/s that a copy reaches: norm and rotation of
-// 16384 tokens of 40 + 8 heads of 128 83 us, 4.9 TB/s, 74 %; of 2001 tokens of 16 + 4
+// 16384 tokens of 40 + 8 heads of 128 82 us, 4.9 TB/s, 75 %; of 2001 tokens of 16 + 4
 // heads of 256 with 64 elements rotated 12 us, 3.4 TB/s; append of 8192 tokens of 8 heads
-// to an E4M3 cache 19 us, 2.6 TB/s, of 4099 with one K head and 32 of q 21 us, 3.3 TB/s;
-// norm and rotation of 8 tokens 3.4 us.  Bound by issue slots and latency together (42 to
+// to an E4M3 cache 18.5 us, 2.7 TB/s, of 4099 with one K head and 32 of q 21 us, 3.4 TB/s;
+// norm and rotation of 8 tokens 3.2 us.  Bound by issue slots and latency together (42 to
 // 60 % of the slots, waits for data the largest stall), the start of a warp first: its
 // token's position, table entry and angles follow one another before its first row can
 // leave.  So a warp keeps one token for as many steps as one round of resident warps
@@ -338,6 +338,8 @@ cudaError_t launch_t(RowsParams p, int sms, cudaStream_t s) {
   const int64_t warps = p.T * ((steps + p.steps_per_warp - 1) / p.steps_per_warp);
   const int64_t grid = (warps + kRowsWarps - 1) / kRowsWarps;
   if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+  // Started beside the kernel before it: append of 64 tokens 4.0 -> 3.7 us, of 8192 19.2 -> 18.5
+  // (2001 tokens of 256 elements 12.1 -> 12.4).
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
