@@ -536,7 +536,8 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
         ok = __all_sync(0xffffffffu, wait(q_full + 8 * h, qphase >> h & 1) && (!both || wait(q_full + 8, qphase >> 1)));
         if (!ok) break;
         qphase ^= both ? 3 : 1 << h;
-        sl2 = fabsf(p.scale_log2) * (r < u.rows ? unscale[h * kTileRows + r] : 1.f);
+        // not 0, however small: a masked score, -inf, has to stay -inf
+        sl2 = fmaxf(fabsf(p.scale_log2) * (r < u.rows ? unscale[h * kTileRows + r] : 1.f), kTinyScale);
         __syncwarp();
         if (lane == 0) {
           tc::arrive(q_empty + 8 * h);

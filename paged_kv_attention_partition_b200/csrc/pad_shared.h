@@ -24,6 +24,7 @@
 namespace pad {
 
 constexpr int kTileRows = 128;  // query rows of one tensor-core tile
+constexpr float kTinyScale = 1.4e-45f;  // the smallest positive fp32: stands in for a score scale of 0
 
 // Query rows of a unit: two tiles, one at D = 256 (whose fp32 accumulator takes
 // half of the tensor memory).

@@ -311,7 +311,7 @@ extern "C" pad_status pad_decode_shared(const pad_tensor *q, const pad_tensor *k
   p.scale_log2 = (float)((double)scale * (double)k_scale * 1.4426950408889634);
   // a scale of 0 weighs every token alike; the smallest positive one does too, and
   // keeps a masked score, -inf, at -inf
-  if (p.scale_log2 == 0.f) p.scale_log2 = 1.4e-45f;
+  if (p.scale_log2 == 0.f) p.scale_log2 = pad::kTinyScale;
   p.v_scale = v_scale;
   p.sinks = sinks != nullptr ? static_cast<const float *>(sinks->data) : nullptr;
   p.out = static_cast<uint16_t *>(out->data);
