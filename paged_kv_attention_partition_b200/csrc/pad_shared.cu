@@ -103,10 +103,13 @@ struct SharedCfg {
 static_assert(sizeof(SharedUnit) <= 64, "queue entry");
 
 // Power of two that scales a row of bf16 q whose largest magnitude is that of either half
-// into f16's range, as an exponent; 0 for a row of zeros or one that is not finite.
+// into f16's range, as an exponent; 0 for a row of zeros or one that is not finite.  From
+// -113 for bf16's largest to 126, above which its inverse is no normal fp32: rows that
+// would take more (below 2^-112) get to 2^0 at least, where f16 holds them to 2^-25 of
+// their largest element.
 __device__ __forceinline__ int q_exponent(uint32_t halves) {
   const uint32_t abs_bits = max(halves & 0xffffu, halves >> 16);
-  return abs_bits == 0 || abs_bits >= 0x7f80u ? 0 : min(100, max(-100, 141 - (int)(abs_bits >> 7)));
+  return abs_bits == 0 || abs_bits >= 0x7f80u ? 0 : min(126, 141 - (int)(abs_bits >> 7));
 }
 // Largest magnitudes of the even and of the odd values so far, a half each.
 __device__ __forceinline__ uint32_t max_abs(uint32_t m, const uint4 &c) {

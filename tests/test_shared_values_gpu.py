@@ -21,3 +21,17 @@ def test_scales_of_either_sign_down_to_zero(cuda_device, scale, kv):
     out, lse = pad.pad_decode_shared(**batch.device(cuda_device), lse=True)
     check(out, lse, batch.reference(), str(scale))
     assert pad.pad_check_device_errors() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("power", [-118, -112, 112, 118])
+def test_query_rows_at_the_ends_of_bf16(cuda_device, kv, power):
+    # rows of 2^power under a scale of 2^-power; one of zeros, and one far smaller than the rest
+    batch = Batch(6, 8, 2, 128, 16, 9, [0, 1, 63, 64, 65, 200], kv=kv, seed=25)
+    batch.q = (batch.q.float().clamp(-3.5, 3.5) * 2.0 ** power).to(torch.bfloat16)
+    batch.q[2, 3] = 0
+    batch.q[4, 1] = 2.0 ** min(power, -100)
+    batch.scale *= 2.0 ** -power
+    out, lse = pad.pad_decode_shared(**batch.device(cuda_device), lse=True)
+    check(out, lse, batch.reference(), str(power))
+    assert pad.pad_check_device_errors() == 0
