@@ -815,15 +815,17 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
         for (int x = 0; x < VEC; ++x) acc[x] += wj[y] * o[y][x];
     }
   }
-  float lse2 = m + log2f(l);  // no token: m = -inf
+  // No weight at all: no token, or scores of -inf alone.  (A row whose scores are NaN has
+  // m = -inf too, as a maximum passes them over, but l is NaN then, and so is its lse.)
+  const bool none = m == -INFINITY && l == 0.f;
+  float lse2 = none ? -INFINITY : m + log2f(l);
   if (p.sinks != nullptr) {
     const float sg = p.sinks[h] * kLog2e;
     const float top = fmaxf(m, sg);
-    const float z = (m == -INFINITY ? 0.f : l * exp2f(m - top)) + (sg == -INFINITY ? 0.f : exp2f(sg - top));
+    const float z = (none ? 0.f : l * exp2f(m - top)) + (sg == -INFINITY ? 0.f : exp2f(sg - top));
     lse2 = top + log2f(z);
   }
-  if (m == -INFINITY && p.sinks == nullptr) lse2 = -INFINITY;
-  const float w = m == -INFINITY ? 0.f : exp2f(m - lse2) * p.v_scale;
+  const float w = none ? 0.f : exp2f(m - lse2) * p.v_scale;
   uint16_t *o = p.out + b * p.o_sb + (int64_t)h * p.o_sh + col;
 #pragma unroll
   for (int i = 0; i < VEC; i += 2)

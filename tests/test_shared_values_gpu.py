@@ -35,3 +35,28 @@ def test_query_rows_at_the_ends_of_bf16(cuda_device, kv, power):
     out, lse = pad.pad_decode_shared(**batch.device(cuda_device), lse=True)
     check(out, lse, batch.reference(), str(power))
     assert pad.pad_check_device_errors() == 0
+
+
+@pytest.mark.parametrize("sink", [None, 0.5])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_scores_that_are_not_numbers(cuda_device, kv, sink):
+    # from a query row (every score), or from one live token's K (one score): that
+    # row's out and lse are NaN, every other row is what it was
+    batch = Batch(7, 8, 2, 128, 16, 12, [9, 0, 100, 64, 1, 5, 30], kv=kv, seed=31, empty=(5,))
+    sinks = None if sink is None else torch.full((8,), sink)
+    ref = batch.reference(sinks)
+    bad = torch.zeros(7, 8, dtype=torch.bool)
+    for b, h in ((0, 0), (1, 2), (4, 7)):
+        batch.q[b, h, 3] = float("nan")
+        bad[b, h] = True
+    batch.k[int(batch.tables[2, 12 + 5]), 1, 7, 11] = float("nan")  # token 192 + 87 of sequence 2, KV head 1
+    bad[2, 4:] = True
+    batch.q[5, 1] = float("nan")  # a padding row is not read
+    out, lse = pad.pad_decode_shared(**batch.device(cuda_device), lse=True,
+                                     sinks=None if sinks is None else sinks.to(cuda_device))
+    on = bad.to(cuda_device)
+    assert bool(out[on].isnan().all()) and bool(lse[on].isnan().all())
+    out[on], ref[0][bad] = 0, 0
+    lse[on], ref[1][bad] = 0, 0
+    check(out, lse, ref, "other rows")
+    assert pad.pad_check_device_errors() == 0
