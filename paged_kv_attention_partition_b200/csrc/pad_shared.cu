@@ -38,7 +38,10 @@ namespace {
 // Every E4M3 code is an f16 value, and q is scaled per row by a power of two that
 // puts its largest element into [2^14, 2^15), where its bf16 values are f16 values
 // too (down to 2^-28 of that element); the row's score scale takes the inverse.  P is
-// f16 then, three bits finer than bf16.
+// f16 then, three bits finer than bf16 down to 2^-14, and a fixed point of 2^-24 below.  So
+// weights stand 2^7 higher than their exponents say (they reach 2^8 over the row's
+// reference, f16 2^15): a weight of 2^-21 of the largest has its full bits, and one is lost
+// from 2^-32 on, with 2^20 of those 2^-12 of the output; 2^-25, without, would be 3 %.
 //
 // A step is (query tile, chunk); step n of the CTA uses S buffer n % NBUF and is the
 // buffer's use n / NBUF, which gives every barrier's phase.  A two-tile unit takes both
@@ -98,6 +101,7 @@ struct SharedCfg {
                             queue = unscale + (F8 ? QR * 4 : 0),
                             bars = queue + kQueue * 64;
   static constexpr uint32_t kBarBytes = 640, total = bars + kBarBytes + 1024 /* alignment slack */;
+  static constexpr float kRaise = F8 ? 7.f : 0.f;       // weights are 2^(s - m + kRaise)
   static constexpr uint32_t kSCol = CT, kOCol = NBUF * CT;  // tensor memory: S buffers, then O
 };
 static_assert(sizeof(SharedUnit) <= 64, "queue entry");
@@ -596,7 +600,7 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
               }
             }
           }
-          const float ref = m == -INFINITY ? 0.f : m;
+          const float ref = (m == -INFINITY ? 0.f : m) - C::kRaise;
           const uint64_t shift = duo(-ref, -ref);
           uint64_t ls[2] = {0, 0};
 #pragma unroll 1
@@ -647,7 +651,7 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
                 dst[i / 4 + x] = make_float4(o[4 * x] * inv, o[4 * x + 1] * inv, o[4 * x + 2] * inv, o[4 * x + 3] * inv);
             }
           }
-          if (r < u.rows) p.lse_part[row] = m + log2f(l);
+          if (r < u.rows) p.lse_part[row] = m - C::kRaise + log2f(l);
           tc::fence_before();
         }
         __syncwarp();

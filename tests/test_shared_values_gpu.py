@@ -60,3 +60,39 @@ def test_scores_that_are_not_numbers(cuda_device, kv, sink):
     lse[on], ref[1][bad] = 0, 0
     check(out, lse, ref, "other rows")
     assert pad.pad_check_device_errors() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D, B", [(64, 600), (256, 300)])
+def test_one_token_before_a_hundred_thousand_others(cuda_device, D, B, kv):
+    # The first token's score is e ln 2 and its value 0; N others have score 0 and value 1:
+    # out = N 2^-e / (1 + N 2^-e).  Units of that whole prefix (more row blocks than CTAs), so
+    # that one running maximum serves every weight.
+    H, bs, n = 64, 256, 512
+    N = n * bs - 1
+    dt = torch.bfloat16 if kv == "bf16" else torch.float8_e4m3fn
+    kc = torch.zeros(2, H, bs, D)
+    vc = torch.ones(2, H, bs, D)
+    kc[0, :, 0, 0], vc[0, :, 0] = 8.0, 0.0
+    q = rand(torch.Generator().manual_seed(1), B, H, D).to(torch.bfloat16)
+    q[..., 0] = (math.log(2) * (16 + torch.arange(H) * 18 / H)).to(torch.bfloat16)  # e of 16 to 34
+    d = lambda t: t.to(cuda_device)
+    shared = torch.ones(n, dtype=torch.int32)
+    shared[0] = 0
+    tables = torch.zeros(1, n, dtype=torch.int32).expand(B, n)
+    out, lse = pad.pad_decode_shared(d(q), d(kc.to(dt)), d(vc.to(dt)), d(shared), d(tables),
+                                     torch.full((B,), n * bs, dtype=torch.int32, device=cuda_device), 0.125, lse=True)
+    s = q[..., 0].double()
+    w = N * torch.exp(-s)
+    want = w / (1 + w)
+    # N like weights: off by half a step of 16 bits (2^-8 bf16; f16 2^-11, or 2^-25 of a fixed point that stands
+    # 2^7 above the largest); N / 16 fp32 additions of them (2^-23 each, if cut off); out's half step; exponentials and
+    # scores of up to 34 below 2^-16
+    tol = want * ((2.0 ** -8 if kv == "bf16" else 2.0 ** -11) + N / 16 * 2.0 ** -23 + 2.0 ** -8 + 2.0 ** -16)
+    if kv == "e4m3":
+        tol = tol + N * 2.0 ** -32
+    err = (out.double().cpu() - want[..., None]).abs()
+    assert (err <= tol[..., None]).all(), float((err / tol[..., None]).max())
+    # l: N / 64 additions in fp32, and a logarithm
+    assert ((lse.double().cpu() - s - torch.log1p(w)).abs() <= N / 64 * 2.0 ** -24 + 2.0 ** -16).all()
+    assert pad.pad_check_device_errors() == 0
