@@ -593,7 +593,7 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
               for (int i = 0; i < D; i += 16) {
                 float o[16];
                 tc::ld16(ocol + i, o);
-                tc::wait_ld();
+                tc::wait_ld16(o);
 #pragma unroll
                 for (int x = 0; x < 16; ++x) o[x] *= a;
                 tc::st16(ocol + i, reinterpret_cast<const uint32_t *>(o));

@@ -96,3 +96,20 @@ def test_one_token_before_a_hundred_thousand_others(cuda_device, D, B, kv):
     # l: N / 64 additions in fp32, and a logarithm
     assert ((lse.double().cpu() - s - torch.log1p(w)).abs() <= N / 64 * 2.0 ** -24 + 2.0 ** -16).all()
     assert pad.pad_check_device_errors() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_maximum_that_rises_with_every_chunk(cuda_device, D, kv):
+    # the sums so far are rescaled, by 2^-9 and more, before every product but a unit's first
+    batch = Batch(5, 8, 2, D, 16, 60, [1, 900, 64, 130, 0], kv=kv, seed=33)
+    batch.scale = 1 / 16.0
+    batch.q[..., 0] = 8 / (16 * batch.k_scale * batch.scale)
+    for pages in [batch.shared] + [row[60:] for row in batch.tables]:
+        for i, page in enumerate(pages.long().tolist()):
+            if page < batch.k.shape[0]:
+                x = batch.k[page, :, :, 0]
+                x[~x.isnan()] = 16.0 * (i // 4 % 16)  # 8 more in the score each chunk
+    out, lse = pad.pad_decode_shared(**batch.device(cuda_device), lse=True)
+    check(out, lse, batch.reference(), "rising")
+    assert pad.pad_check_device_errors() == 0
