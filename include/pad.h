@@ -149,9 +149,11 @@ typedef struct pad_plan {
  * stream) and grown on demand; growing it while `stream` is being captured into
  * a CUDA graph returns PAD_ERR_WORKSPACE (call once outside capture first).
  * Threads: any number of host threads may call at once on different streams
- * (each (device, stream) has its own scratch); calls on the same stream must be
+ * (each (device, stream) has its own scratch, and cudaStreamPerThread is a stream
+ * of each thread); calls on the same stream must be
  * serialised by the caller, as their launches would be unordered anyway (a call
- * may regrow that stream's scratch).
+ * may regrow that stream's scratch).  A stream is idle when it is destroyed:
+ * another that gets its handle gets its scratch.
  */
 pad_status pad_decode(const pad_tensor *q, const pad_tensor *k_cache, const pad_tensor *v_cache,
                       const pad_tensor *block_tables, const pad_tensor *seq_lens, float scale,
@@ -415,8 +417,10 @@ typedef struct pad_shared_plan {
  *  options       NULL, or sinks, k_scale and v_scale as for pad_decode_ex;
  *                window_left must be 0 (PAD_ERR_UNSUPPORTED).
  *  workspace     NULL: the library's, one per (device, stream), grown outside
- *                stream capture only, as for pad_decode; two graphs captured on one
- *                stream share it and must not run at the same time.  Otherwise
+ *                stream capture only, as for pad_decode.  What was captured on a stream
+ *                goes on using that stream's: two graphs captured on one stream must not
+ *                run at the same time, nor a graph beside calls on the stream that it
+ *                was captured on.  Otherwise
  *                256-byte aligned device memory of at least
  *                pad_decode_shared_plan(...).workspace_bytes bytes, any contents, used
  *                by no other call that may run at the same time.

@@ -16,6 +16,8 @@
 #include <mutex>
 #include <new>
 #include <string>
+#include <thread>
+#include <tuple>
 #include <utility>
 #include <vector>
 
@@ -313,13 +315,61 @@ pad_status check_device_ptr(const void *p, int device, const char *name) {
 // counters, zero-filled when (re)allocated and left zero by every launch that
 // completes, so one buffer serves calls of any shape in stream order.
 
+// The driver's id of the stream that this thread means by a handle, unique for the
+// life of the process where a handle is used again after cudaStreamDestroy; 0 if the
+// driver has no such call.  Not for a stream under capture: asking ends the capture.
+typedef CUresult (*StreamGetIdFn)(CUstream, unsigned long long *);
+unsigned long long stream_id(cudaStream_t stream) {
+  static StreamGetIdFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPoint("cuStreamGetId", &f, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<StreamGetIdFn>(f);
+    else
+      cudaGetLastError();
+  });
+  unsigned long long id = 0;
+  return fn != nullptr && fn(stream, &id) == CUDA_SUCCESS ? id : 0;
+}
+
+// Whose a buffer is.  cudaStreamPerThread is one handle for a stream in each host
+// thread, so there the thread belongs to the key.
+struct StreamKey {
+  int device;
+  cudaStream_t stream;
+  std::thread::id thread;
+  StreamKey(int d, cudaStream_t s) : device(d), stream(s) {
+    if (s == cudaStreamPerThread) thread = std::this_thread::get_id();
+  }
+  bool operator<(const StreamKey &o) const {
+    return std::tie(device, stream, thread) < std::tie(o.device, o.stream, o.thread);
+  }
+};
+
 struct Workspace {
   void *ptr = nullptr;
   size_t bytes = 0;
+  unsigned long long id = 0;  // stream_id() of the stream it was last used on
 };
 std::mutex g_ws_mu;
-std::map<std::pair<int, cudaStream_t>, Workspace> g_ws;   // partials
-std::map<std::pair<int, cudaStream_t>, Workspace> g_ctl;  // control blocks
+std::map<StreamKey, Workspace> g_ws;   // partials
+std::map<StreamKey, Workspace> g_ctl;  // control blocks
+
+// Makes a buffer the stream's own, outside capture: when its handle (or its thread's
+// id) is one that a destroyed stream had, that stream's work may still be using the
+// buffer, and is waited for.
+pad_status take_over(Workspace &w, cudaStream_t stream) {
+  const unsigned long long id = stream_id(stream);
+  if (w.ptr != nullptr && w.id != id) {
+    const cudaError_t e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize (scratch)");
+  }
+  w.id = id;
+  return PAD_OK;
+}
 
 // host_scratch's buffers, with whether a stream capture was given one, and the
 // captured ones that a larger buffer has replaced.
@@ -327,20 +377,30 @@ struct Scratch {
   Workspace ws;
   bool captured = false;
 };
-std::map<std::pair<int, cudaStream_t>, Scratch> g_scratch;
+std::map<StreamKey, Scratch> g_scratch;
 std::vector<std::pair<int, void *>> g_scratch_kept;
 
-pad_status get_buffer(std::map<std::pair<int, cudaStream_t>, Workspace> &pool, int device, cudaStream_t stream,
-                      size_t bytes, void **out) {
+pad_status get_buffer(std::map<StreamKey, Workspace> &pool, int device, cudaStream_t stream, size_t bytes, void **out) {
   std::lock_guard<std::mutex> lock(g_ws_mu);
-  Workspace &w = pool[{device, stream}];
-  if (w.bytes >= bytes) {
+  Workspace &w = pool[StreamKey(device, stream)];
+  // (An id costs 0.3 us to ask for, so other streams are taken at their handle here:
+  // one that is destroyed has to be idle.)
+  const bool asks = stream == cudaStreamPerThread;
+  if (w.bytes >= bytes && !asks) {
     *out = w.ptr;
     return PAD_OK;
   }
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
   cudaError_t e = cudaStreamIsCapturing(stream, &cs);
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
+  if (asks && cs == cudaStreamCaptureStatusNone) {
+    const pad_status st = take_over(w, stream);
+    if (st != PAD_OK) return st;
+  }
+  if (w.bytes >= bytes) {
+    *out = w.ptr;
+    return PAD_OK;
+  }
   if (cs != cudaStreamCaptureStatusNone)
     return fail(PAD_ERR_WORKSPACE,
                 "split scratch must grow to %zu bytes while the stream is being captured; "
@@ -605,13 +665,18 @@ pad_status host_scratch(int device, cudaStream_t stream, size_t bytes, void **ou
   std::lock_guard<std::mutex> lock(g_ws_mu);
   Scratch *entry = nullptr;
   try {
-    entry = &g_scratch[{device, stream}];
+    entry = &g_scratch[StreamKey(device, stream)];
     g_scratch_kept.reserve(g_scratch_kept.size() + 1);
   } catch (const std::bad_alloc &) {
     return fail(PAD_ERR_WORKSPACE, "out of host memory");
   }
   Scratch &s = *entry;
-  if (s.ws.bytes < bytes) {
+  const unsigned long long before = s.ws.id;
+  const pad_status st = capturing ? PAD_OK : take_over(s.ws, stream);
+  if (st != PAD_OK) return st;
+  // (a graph of the stream that had this handle before: its buffer is not this stream's)
+  const bool others = s.captured && s.ws.id != before;
+  if (s.ws.bytes < bytes || others) {
     if (capturing)
       return fail(PAD_ERR_WORKSPACE,
                   "scratch must grow to %zu bytes while the stream is being captured; run one call with this shape "
@@ -623,7 +688,9 @@ pad_status host_scratch(int device, cudaStream_t stream, size_t bytes, void **ou
       if ((e = cudaStreamSynchronize(stream)) != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize (scratch)");
       cudaFree(s.ws.ptr);
     }
-    s = Scratch{};
+    s.ws.ptr = nullptr;
+    s.ws.bytes = 0;
+    s.captured = false;
     e = cudaMalloc(&s.ws.ptr, bytes);
     if (e != cudaSuccess) {
       cudaGetLastError();
@@ -830,7 +897,7 @@ pad_status pad_check_device_errors(void *stream_, uint32_t *bits) {
     std::lock_guard<std::mutex> lock(g_ws_mu);
     if ((e = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
     for (auto &kv : g_ctl)
-      if (kv.first.first == device && kv.second.ptr != nullptr) cudaMemset(kv.second.ptr, 0, kv.second.bytes);
+      if (kv.first.device == device && kv.second.ptr != nullptr) cudaMemset(kv.second.ptr, 0, kv.second.bytes);
   }
   if (v != 0)
     return fail(PAD_ERR_DEVICE_CHECK, "kernel saw %s%s%s", (v & pad::kErrBlockId) ? "an out-of-range block id; " : "",
@@ -854,11 +921,11 @@ pad_status pad_release_workspace(int32_t device) {
   if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
   for (auto *pool : {&g_ws, &g_ctl}) {
     for (auto it = pool->begin(); it != pool->end();) {
-      if (device >= 0 && it->first.first != device) {
+      if (device >= 0 && it->first.device != device) {
         ++it;
         continue;
       }
-      if ((e = cudaSetDevice(it->first.first)) != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+      if ((e = cudaSetDevice(it->first.device)) != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
       if ((e = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
       if (it->second.ptr != nullptr) cudaFree(it->second.ptr);
       it = pool->erase(it);
@@ -871,11 +938,11 @@ pad_status pad_release_workspace(int32_t device) {
     return cudaSuccess;
   };
   for (auto it = g_scratch.begin(); it != g_scratch.end();) {
-    if (device >= 0 && it->first.first != device) {
+    if (device >= 0 && it->first.device != device) {
       ++it;
       continue;
     }
-    if (it->second.ws.ptr != nullptr && drop(it->first.first, it->second.ws.ptr) != cudaSuccess)
+    if (it->second.ws.ptr != nullptr && drop(it->first.device, it->second.ws.ptr) != cudaSuccess)
       return cuda_fail(e, "releasing scratch");
     it = g_scratch.erase(it);
   }
