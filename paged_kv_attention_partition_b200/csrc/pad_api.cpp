@@ -372,13 +372,15 @@ pad_status take_over(Workspace &w, cudaStream_t stream) {
 }
 
 // host_scratch's buffers, with whether a stream capture was given one, and the
-// captured ones that a larger buffer has replaced.
+// captured ones that another has replaced.  The map is g_ws_mu's; an entry has a lock
+// of its own, which is taken without g_ws_mu or inside it, never before it.
 struct Scratch {
+  std::mutex mu;
   Workspace ws;
-  bool captured = false;
+  bool captured = false, released = false;
+  std::vector<void *> kept;
 };
-std::map<StreamKey, Scratch> g_scratch;
-std::vector<std::pair<int, void *>> g_scratch_kept;
+std::map<StreamKey, std::shared_ptr<Scratch>> g_scratch;
 
 pad_status get_buffer(std::map<StreamKey, Workspace> &pool, int device, cudaStream_t stream, size_t bytes, void **out) {
   std::lock_guard<std::mutex> lock(g_ws_mu);
@@ -657,16 +659,25 @@ pad_status host_check_shape(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64
 }
 TensorMapEncodeFn host_tensor_map_encoder() { return tensor_map_encoder(); }
 
-pad_status host_scratch(int device, cudaStream_t stream, size_t bytes, void **out) {
+pad_status host_scratch(int device, cudaStream_t stream, size_t bytes, ScratchHold *hold) {
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
   cudaError_t e = cudaStreamIsCapturing(stream, &cs);
   if (e != cudaSuccess) return cuda_fail(e, "cudaStreamIsCapturing");
   const bool capturing = cs != cudaStreamCaptureStatusNone;
-  std::lock_guard<std::mutex> lock(g_ws_mu);
-  Scratch *entry = nullptr;
+  std::shared_ptr<Scratch> entry;
   try {
-    entry = &g_scratch[StreamKey(device, stream)];
-    g_scratch_kept.reserve(g_scratch_kept.size() + 1);
+    do {
+      {
+        std::lock_guard<std::mutex> lock(g_ws_mu);
+        std::shared_ptr<Scratch> &at = g_scratch[StreamKey(device, stream)];
+        if (at == nullptr) at = std::make_shared<Scratch>();
+        entry = at;
+      }
+      if (hold->lock.owns_lock()) hold->lock.unlock();
+      hold->owner = entry;
+      hold->lock = std::unique_lock<std::mutex>(entry->mu);
+    } while (entry->released);  // by a release between the two locks
+    entry->kept.reserve(entry->kept.size() + 1);
   } catch (const std::bad_alloc &) {
     return fail(PAD_ERR_WORKSPACE, "out of host memory");
   }
@@ -682,7 +693,7 @@ pad_status host_scratch(int device, cudaStream_t stream, size_t bytes, void **ou
                   "scratch must grow to %zu bytes while the stream is being captured; run one call with this shape "
                   "outside capture first", bytes);
     if (s.ws.ptr != nullptr && s.captured) {
-      g_scratch_kept.push_back({device, s.ws.ptr});
+      s.kept.push_back(s.ws.ptr);
     } else if (s.ws.ptr != nullptr) {
       // queued work on this stream may still use the old buffer
       if ((e = cudaStreamSynchronize(stream)) != cudaSuccess) return cuda_fail(e, "cudaStreamSynchronize (scratch)");
@@ -700,7 +711,7 @@ pad_status host_scratch(int device, cudaStream_t stream, size_t bytes, void **ou
     s.ws.bytes = bytes;
   }
   s.captured = s.captured || capturing;
-  *out = s.ws.ptr;
+  hold->ptr = s.ws.ptr;
   return PAD_OK;
 }
 
@@ -931,29 +942,23 @@ pad_status pad_release_workspace(int32_t device) {
       it = pool->erase(it);
     }
   }
-  auto drop = [&](int d, void *ptr) -> cudaError_t {
-    if ((e = cudaSetDevice(d)) != cudaSuccess) return e;
-    if ((e = cudaDeviceSynchronize()) != cudaSuccess) return e;
-    cudaFree(ptr);
-    return cudaSuccess;
-  };
   for (auto it = g_scratch.begin(); it != g_scratch.end();) {
     if (device >= 0 && it->first.device != device) {
       ++it;
       continue;
     }
-    if (it->second.ws.ptr != nullptr && drop(it->first.device, it->second.ws.ptr) != cudaSuccess)
-      return cuda_fail(e, "releasing scratch");
-    it = g_scratch.erase(it);
-  }
-  for (size_t i = 0; i < g_scratch_kept.size();) {
-    if (device >= 0 && g_scratch_kept[i].first != device) {
-      ++i;
-      continue;
+    {
+      Scratch &s = *it->second;
+      std::lock_guard<std::mutex> held(s.mu);
+      if ((e = cudaSetDevice(it->first.device)) != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+      if ((e = cudaDeviceSynchronize()) != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
+      if (s.ws.ptr != nullptr) cudaFree(s.ws.ptr);
+      for (void *p : s.kept) cudaFree(p);
+      s.ws = Workspace{};
+      s.kept.clear();
+      s.released = true;  // (a call that found it before it left the map looks again)
     }
-    if (drop(g_scratch_kept[i].first, g_scratch_kept[i].second) != cudaSuccess)
-      return cuda_fail(e, "releasing scratch");
-    g_scratch_kept.erase(g_scratch_kept.begin() + (long)i);
+    it = g_scratch.erase(it);
   }
   if ((e = cudaSetDevice(cur)) != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
   return PAD_OK;

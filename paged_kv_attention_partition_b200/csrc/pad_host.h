@@ -7,6 +7,9 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <memory>
+#include <mutex>
+
 #include "pad.h"
 
 namespace pad {
@@ -28,7 +31,16 @@ pad_status host_check_shape(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int64
 // arbitrary; freed by pad_release_workspace.  It grows outside stream capture
 // only, and a buffer that a capture has seen is kept, not freed, when a larger
 // one replaces it: the captured graph still uses it.
-pad_status host_scratch(int device, cudaStream_t stream, size_t bytes, void **out);
+//
+// The caller holds it until `hold` goes: a thread that wants the same stream's waits,
+// so that one call's kernels stay together, and so does a release.  Other streams'
+// are not waited for.
+struct ScratchHold {
+  void *ptr = nullptr;
+  std::shared_ptr<void> owner;
+  std::unique_lock<std::mutex> lock;  // (released before its owner)
+};
+pad_status host_scratch(int device, cudaStream_t stream, size_t bytes, ScratchHold *hold);
 
 typedef CUresult (*TensorMapEncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                       const cuuint64_t *, const cuuint32_t *, const cuuint32_t *,

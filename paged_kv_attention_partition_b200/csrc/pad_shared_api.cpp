@@ -4,8 +4,6 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
-#include <mutex>
-
 #include "pad.h"
 #include "pad_host.h"
 #include "pad_internal.h"
@@ -322,11 +320,15 @@ extern "C" pad_status pad_decode_shared(const pad_tensor *q, const pad_tensor *k
   p.lse_sh = lse != nullptr ? lse->stride[1] : 0;
   cudaError_t e = pad::device_error_word(device, &p.err);
   if (e != cudaSuccess) return pad::host_cuda_fail(e, "error word");
-  // Two threads on one stream share its scratch: neither's kernels between the
-  // other's two, nor a larger buffer between the other's look and its launches.
-  static std::mutex launches;
-  std::lock_guard<std::mutex> lock(launches);
-  if (workspace == nullptr && (st = pad::host_scratch(device, stream, l.total, &workspace)) != PAD_OK) return st;
+  // Two threads on one stream share its scratch, held over the launches: neither's kernels
+  // between the other's two, nor a larger buffer between the other's look and its launches.
+  // (A workspace of the caller's needs no lock: another call's kernel between the two only
+  // adds to what the merge waits for.)
+  pad::ScratchHold scratch;
+  if (workspace == nullptr) {
+    if ((st = pad::host_scratch(device, stream, l.total, &scratch)) != PAD_OK) return st;
+    workspace = scratch.ptr;
+  }
   char *base = static_cast<char *>(workspace);
   p.o_part = reinterpret_cast<float *>(base + l.o_part);
   p.lse_part = reinterpret_cast<float *>(base + l.lse_part);

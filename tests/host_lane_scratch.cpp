@@ -14,7 +14,9 @@
 #undef main
 #undef cudaGetDriverEntryPoint
 
+#include <algorithm>
 #include <atomic>
+#include <chrono>
 #include <condition_variable>
 #include <map>
 #include <mutex>
@@ -35,19 +37,38 @@ static CUresult fake_stream_id(CUstream s, unsigned long long *id) {
   *id = s == cudaStreamPerThread ? mine : stream_ids.count(s) ? stream_ids[s] : 1 + (unsigned long long)(uintptr_t)s;
   return CUDA_SUCCESS;
 }
+// (the lane's encoder records what it is asked for: one thread at a time)
+static CUresult locked_encode(CUtensorMap *map, CUtensorMapDataType dt, cuuint32_t rank, void *addr,
+                              const cuuint64_t *dims, const cuuint64_t *strides, const cuuint32_t *box,
+                              const cuuint32_t *elem, CUtensorMapInterleave il, CUtensorMapSwizzle sw,
+                              CUtensorMapL2promotion l2, CUtensorMapFloatOOBfill oob) {
+  static std::mutex mu;
+  std::lock_guard<std::mutex> lock(mu);
+  return fake_encode(map, dt, rank, addr, dims, strides, box, elem, il, sw, l2, oob);
+}
 cudaError_t cudaGetDriverEntryPoint(const char *sym, void **fn, unsigned long long flags,
                                     enum cudaDriverEntryPointQueryResult *q) {
-  if (no_ids || strcmp(sym, "cuStreamGetId") != 0) return fake_lane_entry_point(sym, fn, flags, q);
-  *fn = reinterpret_cast<void *>(&fake_stream_id);
+  const bool id = strcmp(sym, "cuStreamGetId") == 0;
+  if (id ? no_ids : strcmp(sym, "cuTensorMapEncodeTiled") != 0) return fake_lane_entry_point(sym, fn, flags, q);
+  *fn = id ? reinterpret_cast<void *>(&fake_stream_id) : reinterpret_cast<void *>(&locked_encode);
   if (q) *q = cudaDriverEntryPointSuccess;
   return cudaSuccess;
 }
 
-// The shared decode's launches are recorded.
+// The shared decode's launches are recorded; while `meet` is set each waits until that
+// many are under way at once, or half a second.
+static std::mutex shared_mu;
+static std::condition_variable shared_cv;
 static std::vector<std::pair<pad::SharedParams, cudaStream_t>> shared_launches;
+static int now_inside = 0, most_inside = 0, meet = 0;
 namespace pad {
 cudaError_t launch_shared(const SharedParams &p, int, bool, cudaStream_t s) {
+  std::unique_lock<std::mutex> lock(shared_mu);
   shared_launches.push_back({p, s});
+  most_inside = std::max(most_inside, ++now_inside);
+  shared_cv.notify_all();
+  if (meet > 0) shared_cv.wait_for(lock, std::chrono::milliseconds(500), [] { return most_inside >= meet; });
+  --now_inside;
   return cudaSuccess;
 }
 }  // namespace pad
@@ -159,6 +180,52 @@ static void under_capture_no_id_is_asked_for() {
   CHECK(pad_release_workspace(-1) == PAD_OK && fake::library_live() == 0, "released");
 }
 
+// How many calls of two threads are between their two kernels at once.
+template <class Call>
+static int at_once(Call call) {
+  most_inside = 0;
+  meet = 2;
+  std::thread a([&] { CHECK(call(0) == PAD_OK, "%s", pad_last_error()); });
+  std::thread b([&] { CHECK(call(1) == PAD_OK, "%s", pad_last_error()); });
+  a.join();
+  b.join();
+  meet = 0;
+  return most_inside;
+}
+
+static void only_one_streams_calls_wait_for_one_another() {
+  SharedProblem p[2];
+  void *streams[2] = {reinterpret_cast<void *>(0x70), reinterpret_cast<void *>(0x80)};
+  pad_shared_plan plan;
+  CHECK(pad_decode_shared_plan(4, 8, 2, 128, 16, 8, 4, PAD_BF16, 0, &plan) == PAD_OK, "plan");
+  const size_t bytes = (size_t)plan.workspace_bytes;
+  void *ws[2] = {fake::device_buffer(bytes), fake::device_buffer(bytes)};
+  for (int i = 0; i < 2; ++i) CHECK(p[i].shared(streams[i]) == PAD_OK, "%s", pad_last_error());  // scratch exists
+  CHECK(at_once([&](int i) { return p[i].shared(streams[i]); }) == 2, "two streams");
+  CHECK(at_once([&](int i) { return p[i].shared(streams[0], ws[i], bytes); }) == 2, "workspaces of the callers");
+  CHECK(at_once([&](int i) { return p[i].shared(streams[0]); }) == 1, "one stream's scratch");
+  // a release waits for the call that holds the scratch
+  meet = 2;
+  most_inside = 0;
+  std::thread call([&] { CHECK(p[0].shared(streams[0]) == PAD_OK, "%s", pad_last_error()); });
+  {
+    std::unique_lock<std::mutex> lock(shared_mu);
+    shared_cv.wait(lock, [] { return now_inside == 1; });
+  }
+  std::thread release([&] { CHECK(pad_release_workspace(-1) == PAD_OK, "%s", pad_last_error()); });
+  std::this_thread::sleep_for(std::chrono::milliseconds(100));
+  {
+    std::lock_guard<std::mutex> lock(shared_mu);
+    CHECK(now_inside == 1, "the call is over already");
+    CHECK(fake::find(shared_launches.back().first.o_part) != nullptr, "freed under a call");
+  }
+  call.join();
+  release.join();
+  meet = 0;
+  CHECK(fake::library_live() == 0, "released");
+  CHECK(p[0].shared(streams[0]) == PAD_OK && pad_release_workspace(-1) == PAD_OK && fake::library_live() == 0, "again");
+}
+
 int main(int argc, char **argv) {
   const std::string what = argc > 1 ? argv[1] : "";
   no_ids = argc > 2 && std::string(argv[2]) == "no-ids";
@@ -166,6 +233,7 @@ int main(int argc, char **argv) {
   else if (what == "reuse") a_handle_that_comes_back();
   else if (what == "thread-reuse") a_thread_id_that_comes_back();
   else if (what == "capture") under_capture_no_id_is_asked_for();
+  else if (what == "locks") only_one_streams_calls_wait_for_one_another();
   else return 2;
   if (failures) return 1;
   puts("clean");

@@ -49,3 +49,31 @@ def test_two_threads_on_their_default_streams(cuda_device):
         check(a["out"], a["lse"], ref, "shared")
         check(o, l, ref, "pad_decode")
     assert pad.pad_check_device_errors() == 0
+
+
+def test_two_threads_with_workspaces_on_one_stream(cuda_device):
+    # nothing of the library's is shared, so their kernels may come between one another's
+    batches = [Batch(B, 8, 2, 128, 16, 30, [5 * i for i in range(B)], seed=s) for B, s in ((4, 44), (30, 45))]
+    args = [b.device(cuda_device) for b in batches]
+    for b, a in zip(batches, args):
+        need = pad.pad_decode_shared_plan(len(b.lens), 8, 2, 128, 16, b.W, 30)["workspace_bytes"]
+        a["workspace"] = torch.empty(need, dtype=torch.uint8, device=cuda_device)
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [[], []]
+
+    def work(i):
+        for _ in range(40):
+            o = torch.empty_like(args[i]["q"])
+            pad.pad_decode_shared(**args[i], out=o, stream=stream)
+            got[i].append(o)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    for b, results in zip(batches, got):
+        assert len(results) == 40
+        ref = b.reference()
+        check(results[0], None, ref, "first")
+        assert all(torch.equal(results[0], r) for r in results[1:])

@@ -48,3 +48,7 @@ def test_each_thread_has_its_own_scratch_on_the_per_thread_stream(lane, ids):
 @pytest.mark.parametrize("scenario", ["reuse", "thread-reuse", "capture"])
 def test_scratch_of_streams_that_are_gone(lane, scenario):
     run_lane(lane, scenario)
+
+
+def test_only_calls_that_share_scratch_wait_for_one_another(lane):
+    run_lane(lane, "locks")
