@@ -319,7 +319,12 @@ def pad_decode_with_workspace(q, k_cache, v_cache, block_tables, seq_lens, scale
 
 # The calls below go through _pad_torch.so (csrc/pad_torch.cpp), which packs the
 # descriptors and allocates the outputs: a decode step makes several of them per
-# layer, and marshalling them from here costs more than their launches.
+# layer, and marshalling them from here costs more than their launches.  On a
+# ``stream`` other than torch's current one they allocate what they return on that
+# stream and make it known to torch's allocator for every tensor of the call, so that
+# tensors may be dropped as soon as the call returns (the order of the streams is the
+# caller's).  On cudaStreamPerThread, which the allocator cannot follow, outputs must be
+# given and all tensors outlive the work.
 _fast = None
 
 

@@ -13,6 +13,7 @@
 #include <ATen/Functions.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -71,12 +72,6 @@ const at::Tensor &cuda_tensor(PyObject *o, const char *name) {
 at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type, const at::Tensor &like) {
   return at::detail::empty_cuda(sizes, type, like.device(), c10::nullopt);  // (past the dispatcher: half its time)
 }
-// An output: the caller's tensor, or a contiguous one of the shape and type of `like`.
-at::Tensor output(PyObject *o, const at::Tensor &like, const char *name) {
-  if (o == Py_None) return empty(like.sizes(), like.scalar_type(), like);
-  return cuda_tensor(o, name);
-}
-
 float number(PyObject *o) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) throw python_error();
@@ -93,10 +88,50 @@ void *handle(PyObject *o) {
   return p;
 }
 
-// A stream's handle; None: the current one of the tensor's device.
-void *handle(PyObject *o, const at::Tensor &on) {
-  return o == Py_None ? c10::cuda::getCurrentCUDAStream(on.get_device()).stream() : handle(o);
-}
+// The stream of a call: torch's current one of the tensor's device (None), or one given
+// beside it.  torch's allocator gives a block out again in the order of the stream that it
+// was allocated on, so a stream beside that has to be made known to it: outputs come from
+// the call's stream and are marked for the current one, where the caller goes on with
+// them; the caller's tensors are marked for the call's.
+class On {
+ public:
+  On(PyObject *o, const at::Tensor &t)
+      : current_(c10::cuda::getCurrentCUDAStream(t.get_device())), call_(current_), handle_(current_.stream()) {
+    if (o == Py_None) return;
+    handle_ = handle(o);
+    cudaStream_t s = static_cast<cudaStream_t>(handle_);
+    if (s == cudaStreamLegacy) s = nullptr;
+    // (one handle for a stream in every thread: an event that the allocator records on
+    // it when it frees a block may be another thread's)
+    unknown_ = s == cudaStreamPerThread;
+    beside_ = !unknown_ && s != current_.stream();
+    if (beside_) call_ = c10::cuda::getStreamFromExternal(s, t.get_device());
+  }
+  void *stream() const { return handle_; }
+  at::Tensor allocate(at::IntArrayRef sizes, at::ScalarType type, const at::Tensor &like) const {
+    TORCH_CHECK_VALUE(!unknown_, "on cudaStreamPerThread the outputs must be given: torch's allocator cannot follow it");
+    if (!beside_) return empty(sizes, type, like);
+    c10::cuda::CUDAStreamGuard guard(call_);
+    at::Tensor t = empty(sizes, type, like);
+    c10::cuda::CUDACachingAllocator::recordStream(t.storage().data_ptr(), current_);
+    return t;
+  }
+  // An output: the caller's tensor, or a contiguous one of the shape and type of `like`.
+  at::Tensor output(PyObject *o, const at::Tensor &like, const char *name) const {
+    return o == Py_None ? allocate(like.sizes(), like.scalar_type(), like) : cuda_tensor(o, name);
+  }
+  // The call's arguments, once it is launched.
+  void used(PyObject *const *a, Py_ssize_t n) const {
+    if (!beside_) return;
+    for (Py_ssize_t i = 0; i < n; ++i)
+      if (THPVariable_Check(a[i])) c10::cuda::CUDACachingAllocator::recordStream(THPVariable_Unpack(a[i]).storage().data_ptr(), call_);
+  }
+
+ private:
+  c10::cuda::CUDAStream current_, call_;
+  void *handle_;
+  bool beside_ = false, unknown_ = false;
+};
 
 void expect(Py_ssize_t n, Py_ssize_t want) { TORCH_CHECK_TYPE(n == want, "expected ", want, " arguments, got ", n); }
 
@@ -128,21 +163,22 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   expect(n, 11);
   const at::Tensor &q = cuda_tensor(a[0], "q");
-  c10::cuda::CUDAGuard on(q.device());
-  at::Tensor q_out = output(a[8], q, "q_out"), k_out;
-  if (a[1] != Py_None) k_out = output(a[9], cuda_tensor(a[1], "k"), "k_out");
+  c10::cuda::CUDAGuard device(q.device());
+  const On on(a[10], q);
+  at::Tensor q_out = on.output(a[8], q, "q_out"), k_out;
+  if (a[1] != Py_None) k_out = on.output(a[9], cuda_tensor(a[1], "k"), "k_out");
   else if (a[9] != Py_None) k_out = cuda_tensor(a[9], "k_out");
   if (q.numel() > 0) {  // no token: no data pointers either
     Desc dq(a[0], "q"), dk(a[1], "k"), dqw(a[2], "q_weight"), dkw(a[3], "k_weight"), dp(a[4], "positions"),
         df(a[5], "inv_freq"), dqo(q_out, "q_out"), dko(k_out, "k_out");
     const float eps = number(a[6]);
     const int inter = truth(a[7]);
-    void *stream = handle(a[10], q);
     const pad_status st = without_gil([&] {
       return g_norm_rope(dq.address(), dk.address(), dqw.address(), dkw.address(), eps, dp.address(), df.address(), inter,
-                         dqo.address(), dko.address(), stream);
+                         dqo.address(), dko.address(), on.stream());
     });
     if (st != PAD_OK) return PyLong_FromLong(st);
+    on.used(a, n);
   }
   PyObject *x = wrap(q_out), *y = wrap(k_out);
   PyObject *r = x != nullptr && y != nullptr ? PyTuple_Pack(2, x, y) : nullptr;
@@ -158,10 +194,11 @@ PyObject *append_kv(PyObject *, PyObject *const *a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   expect(n, 17);
   const at::Tensor &k = cuda_tensor(a[0], "k");
-  c10::cuda::CUDAGuard on(k.device());
+  c10::cuda::CUDAGuard device(k.device());
+  const On on(a[16], k);
   TORCH_CHECK_VALUE(a[11] != Py_None || a[13] == Py_None, "q_out without q");
   at::Tensor q_out;
-  if (a[11] != Py_None) q_out = output(a[13], cuda_tensor(a[11], "q"), "q_out");
+  if (a[11] != Py_None) q_out = on.output(a[13], cuda_tensor(a[11], "q"), "q_out");
   if (k.numel() > 0) {
     Desc dk(a[0], "k"), dv(a[1], "v"), dp(a[2], "positions"), dt(a[3], "block_tables"), dkc(a[4], "k_cache"),
         dvc(a[5], "v_cache"), ds(a[6], "seq_ids"), df(a[7], "inv_freq"), dkw(a[9], "k_weight"), dq(a[11], "q"),
@@ -176,12 +213,12 @@ PyObject *append_kv(PyObject *, PyObject *const *a, Py_ssize_t n) {
     o.q_out = dqo.address();
     o.k_scale = number(a[14]);
     o.v_scale = number(a[15]);
-    void *stream = handle(a[16], k);
     const pad_status st = without_gil([&] {
       return g_append(dk.address(), dv.address(), dp.address(), ds.address(), dt.address(), &o, dkc.address(),
-                      dvc.address(), stream);
+                      dvc.address(), on.stream());
     });
     if (st != PAD_OK) return PyLong_FromLong(st);
+    on.used(a, n);
   }
   return wrap(q_out);
   END_HANDLE_TH_ERRORS
@@ -193,11 +230,12 @@ PyObject *decode_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   expect(n, 14);
   const at::Tensor &q = cuda_tensor(a[0], "q");
-  c10::cuda::CUDAGuard on(q.device());
-  at::Tensor out = output(a[7], q, "out"), lse;
+  c10::cuda::CUDAGuard device(q.device());
+  const On on(a[13], q);
+  at::Tensor out = on.output(a[7], q, "out"), lse;
   if (a[8] == Py_True) {
     TORCH_CHECK_VALUE(q.dim() >= 2, "q must be [B, Hq, D]");
-    lse = empty({q.size(0), q.size(1)}, at::kFloat, q);
+    lse = on.allocate({q.size(0), q.size(1)}, at::kFloat, q);
   } else if (a[8] != Py_None && a[8] != Py_False) {
     lse = cuda_tensor(a[8], "lse");
   }
@@ -218,12 +256,12 @@ PyObject *decode_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
       ws = w.data_ptr();
       ws_bytes = w.numel() * w.element_size();
     }
-    void *stream = handle(a[13], q);
     const pad_status st = without_gil([&] {
       return g_shared(dq.address(), dk.address(), dv.address(), dsh.address(), dt.address(), dl.address(), scale, &o,
-                      dout.address(), dlse.address(), ws, ws_bytes, stream);
+                      dout.address(), dlse.address(), ws, ws_bytes, on.stream());
     });
     if (st != PAD_OK) return PyLong_FromLong(st);
+    on.used(a, n);
   }
   PyObject *x = wrap(out), *y = wrap(lse);
   PyObject *r = x != nullptr && y != nullptr ? PyTuple_Pack(2, x, y) : nullptr;

@@ -77,3 +77,77 @@ def test_two_threads_with_workspaces_on_one_stream(cuda_device):
         ref = b.reference()
         check(results[0], None, ref, "first")
         assert all(torch.equal(results[0], r) for r in results[1:])
+
+
+def rows_call(dev, stream, **kw):
+    x = torch.randn(3001, 12, 128, device=dev).to(torch.bfloat16)
+    return [x], lambda: pad.pad_qk_norm_rope(x[:, :8], x[:, 8:], stream=stream, **kw)
+
+
+def append_call(dev, stream, **kw):
+    x = torch.randn(3001, 12, 128, device=dev).to(torch.bfloat16)
+    pos = torch.arange(3001, dtype=torch.int32, device=dev)
+    tables = torch.arange(188, dtype=torch.int32, device=dev).view(1, 188)
+    kc, vc = (torch.zeros(188, 2, 16, 128, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    return [x, kc, vc], lambda: [pad.pad_append_kv(x[:, 8:10], x[:, 10:], pos, tables, kc, vc,
+                                                   seq_ids=torch.zeros_like(pos), q=x[:, :8], stream=stream, **kw)]
+
+
+def shared_call(dev, stream, **kw):
+    batch = Batch(260, 64, 2, 128, 16, 30, [i % 7 for i in range(260)], seed=46)
+    a = batch.device(dev)
+    return [a["q"], a["k_cache"], a["v_cache"]], lambda: pad.pad_decode_shared(**a, lse=True, stream=stream, **kw)
+
+
+@pytest.mark.parametrize("make", [rows_call, append_call, shared_call])
+def test_tensors_dropped_while_another_stream_uses_them(cuda_device, make):
+    # a block that the side stream still reads or writes is not given out again
+    side, main = torch.cuda.Stream(), torch.cuda.current_stream()
+    tensors, call = make(cuda_device, side)
+    call()  # (scratch, modules)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(400_000_000)
+    outs = [t for t in call() if t is not None]
+    held = {t.untyped_storage().data_ptr() for t in tensors + outs}
+    sizes = [t.untyped_storage().nbytes() for t in tensors + outs for _ in range(3)]
+    del tensors, outs, call
+    fresh = [torch.empty(n, dtype=torch.uint8, device=cuda_device) for n in sizes]
+    assert not side.query(), "the side stream was done too soon to see anything"
+    assert not held & {t.untyped_storage().data_ptr() for t in fresh}
+    side.synchronize()
+
+
+@pytest.mark.parametrize("make", [rows_call, append_call, shared_call])
+def test_outputs_dropped_while_the_current_stream_reads_them(cuda_device, make):
+    side, main = torch.cuda.Stream(), torch.cuda.current_stream()
+    tensors, call = make(cuda_device, side)
+    first = call()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in first if t is not None]
+    side.wait_stream(main)
+    outs = [t for t in call() if t is not None]
+    main.wait_stream(side)
+    torch.cuda._sleep(400_000_000)
+    copies = [t.clone() for t in outs]
+    held, sizes = {t.data_ptr() for t in outs}, [t.untyped_storage().nbytes() for t in outs]
+    del outs
+    with torch.cuda.stream(side):
+        fresh = [torch.empty(n, dtype=torch.uint8, device=cuda_device).fill_(0xFF) for n in sizes for _ in range(3)]
+    assert not main.query(), "the current stream was done too soon to see anything"
+    assert not held & {t.data_ptr() for t in fresh}
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(copies, want))
+
+
+def test_the_per_thread_stream_takes_given_outputs_only(cuda_device):
+    for make in (rows_call, append_call, shared_call):
+        _, call = make(cuda_device, PER_THREAD)
+        with pytest.raises(ValueError):
+            call()
+    x = torch.randn(5, 4, 128, device=cuda_device).to(torch.bfloat16)
+    out = torch.empty_like(x)
+    torch.cuda.synchronize()
+    got, _ = pad.pad_qk_norm_rope(x, None, q_out=out, stream=PER_THREAD)
+    torch.cuda.synchronize()
+    assert got is out and torch.equal(out, x)
