@@ -27,6 +27,10 @@ decltype(&pad_qk_norm_rope) g_norm_rope = nullptr;
 decltype(&pad_append_kv) g_append = nullptr;
 decltype(&pad_decode_shared) g_shared = nullptr;
 
+// torch gives a tensor without elements no address, and the library takes null for no
+// tensor (or refuses it): any other will do, as nothing reads it.
+void *address_of(const at::Tensor &t) { return t.numel() == 0 ? reinterpret_cast<void *>(256) : t.data_ptr(); }
+
 // The descriptor of an optional tensor argument; address() is null for None.
 class Desc {
  public:
@@ -43,7 +47,7 @@ class Desc {
  private:
   void set(const at::Tensor &t, const char *name) {
     some_ = true;
-    d_.data = t.data_ptr();
+    d_.data = address_of(t);
     switch (t.scalar_type()) {
       case at::kBFloat16: d_.dtype = PAD_BF16; break;
       case at::kFloat: d_.dtype = PAD_F32; break;
@@ -168,18 +172,16 @@ PyObject *qk_norm_rope(PyObject *, PyObject *const *a, Py_ssize_t n) {
   at::Tensor q_out = on.output(a[8], q, "q_out"), k_out;
   if (a[1] != Py_None) k_out = on.output(a[9], cuda_tensor(a[1], "k"), "k_out");
   else if (a[9] != Py_None) k_out = cuda_tensor(a[9], "k_out");
-  if (q.numel() > 0) {  // no token: no data pointers either
-    Desc dq(a[0], "q"), dk(a[1], "k"), dqw(a[2], "q_weight"), dkw(a[3], "k_weight"), dp(a[4], "positions"),
-        df(a[5], "inv_freq"), dqo(q_out, "q_out"), dko(k_out, "k_out");
-    const float eps = number(a[6]);
-    const int inter = truth(a[7]);
-    const pad_status st = without_gil([&] {
-      return g_norm_rope(dq.address(), dk.address(), dqw.address(), dkw.address(), eps, dp.address(), df.address(), inter,
-                         dqo.address(), dko.address(), on.stream());
-    });
-    if (st != PAD_OK) return PyLong_FromLong(st);
-    on.used(a, n);
-  }
+  Desc dq(a[0], "q"), dk(a[1], "k"), dqw(a[2], "q_weight"), dkw(a[3], "k_weight"), dp(a[4], "positions"),
+      df(a[5], "inv_freq"), dqo(q_out, "q_out"), dko(k_out, "k_out");
+  const float eps = number(a[6]);
+  const int inter = truth(a[7]);
+  const pad_status st = without_gil([&] {
+    return g_norm_rope(dq.address(), dk.address(), dqw.address(), dkw.address(), eps, dp.address(), df.address(), inter,
+                       dqo.address(), dko.address(), on.stream());
+  });
+  if (st != PAD_OK) return PyLong_FromLong(st);
+  on.used(a, n);
   PyObject *x = wrap(q_out), *y = wrap(k_out);
   PyObject *r = x != nullptr && y != nullptr ? PyTuple_Pack(2, x, y) : nullptr;
   Py_XDECREF(x);
@@ -199,27 +201,25 @@ PyObject *append_kv(PyObject *, PyObject *const *a, Py_ssize_t n) {
   TORCH_CHECK_VALUE(a[11] != Py_None || a[13] == Py_None, "q_out without q");
   at::Tensor q_out;
   if (a[11] != Py_None) q_out = on.output(a[13], cuda_tensor(a[11], "q"), "q_out");
-  if (k.numel() > 0) {
-    Desc dk(a[0], "k"), dv(a[1], "v"), dp(a[2], "positions"), dt(a[3], "block_tables"), dkc(a[4], "k_cache"),
-        dvc(a[5], "v_cache"), ds(a[6], "seq_ids"), df(a[7], "inv_freq"), dkw(a[9], "k_weight"), dq(a[11], "q"),
-        dqw(a[12], "q_weight"), dqo(q_out, "q_out");
-    pad_append_options o{};
-    o.inv_freq = df.address();
-    o.interleaved = truth(a[8]);
-    o.k_weight = dkw.address();
-    o.eps = number(a[10]);
-    o.q = dq.address();
-    o.q_weight = dqw.address();
-    o.q_out = dqo.address();
-    o.k_scale = number(a[14]);
-    o.v_scale = number(a[15]);
-    const pad_status st = without_gil([&] {
-      return g_append(dk.address(), dv.address(), dp.address(), ds.address(), dt.address(), &o, dkc.address(),
-                      dvc.address(), on.stream());
-    });
-    if (st != PAD_OK) return PyLong_FromLong(st);
-    on.used(a, n);
-  }
+  Desc dk(a[0], "k"), dv(a[1], "v"), dp(a[2], "positions"), dt(a[3], "block_tables"), dkc(a[4], "k_cache"),
+      dvc(a[5], "v_cache"), ds(a[6], "seq_ids"), df(a[7], "inv_freq"), dkw(a[9], "k_weight"), dq(a[11], "q"),
+      dqw(a[12], "q_weight"), dqo(q_out, "q_out");
+  pad_append_options o{};
+  o.inv_freq = df.address();
+  o.interleaved = truth(a[8]);
+  o.k_weight = dkw.address();
+  o.eps = number(a[10]);
+  o.q = dq.address();
+  o.q_weight = dqw.address();
+  o.q_out = dqo.address();
+  o.k_scale = number(a[14]);
+  o.v_scale = number(a[15]);
+  const pad_status st = without_gil([&] {
+    return g_append(dk.address(), dv.address(), dp.address(), ds.address(), dt.address(), &o, dkc.address(),
+                    dvc.address(), on.stream());
+  });
+  if (st != PAD_OK) return PyLong_FromLong(st);
+  on.used(a, n);
   return wrap(q_out);
   END_HANDLE_TH_ERRORS
 }
@@ -239,30 +239,28 @@ PyObject *decode_shared(PyObject *, PyObject *const *a, Py_ssize_t n) {
   } else if (a[8] != Py_None && a[8] != Py_False) {
     lse = cuda_tensor(a[8], "lse");
   }
-  if (q.numel() > 0) {
-    Desc dq(a[0], "q"), dk(a[1], "k_cache"), dv(a[2], "v_cache"), dsh(a[3], "shared_table"), dt(a[4], "block_tables"),
-        dl(a[5], "seq_lens"), dout(out, "out"), dlse(lse, "lse"), dsk(a[9], "sinks");
-    const float scale = number(a[6]);
-    pad_decode_options o{};
-    o.sinks = dsk.address();
-    o.k_scale = number(a[10]);
-    o.v_scale = number(a[11]);
-    void *ws = nullptr;
-    size_t ws_bytes = 0;
-    if (a[12] != Py_None) {
-      const at::Tensor &w = cuda_tensor(a[12], "workspace");
-      TORCH_CHECK_VALUE(w.device() == q.device() && w.is_contiguous(),
-                        "workspace must be a contiguous tensor on q's device");
-      ws = w.data_ptr();
-      ws_bytes = w.numel() * w.element_size();
-    }
-    const pad_status st = without_gil([&] {
-      return g_shared(dq.address(), dk.address(), dv.address(), dsh.address(), dt.address(), dl.address(), scale, &o,
-                      dout.address(), dlse.address(), ws, ws_bytes, on.stream());
-    });
-    if (st != PAD_OK) return PyLong_FromLong(st);
-    on.used(a, n);
+  Desc dq(a[0], "q"), dk(a[1], "k_cache"), dv(a[2], "v_cache"), dsh(a[3], "shared_table"), dt(a[4], "block_tables"),
+      dl(a[5], "seq_lens"), dout(out, "out"), dlse(lse, "lse"), dsk(a[9], "sinks");
+  const float scale = number(a[6]);
+  pad_decode_options o{};
+  o.sinks = dsk.address();
+  o.k_scale = number(a[10]);
+  o.v_scale = number(a[11]);
+  void *ws = nullptr;
+  size_t ws_bytes = 0;
+  if (a[12] != Py_None) {
+    const at::Tensor &w = cuda_tensor(a[12], "workspace");
+    TORCH_CHECK_VALUE(w.device() == q.device() && w.is_contiguous(),
+                      "workspace must be a contiguous tensor on q's device");
+    ws = address_of(w);
+    ws_bytes = w.numel() * w.element_size();
   }
+  const pad_status st = without_gil([&] {
+    return g_shared(dq.address(), dk.address(), dv.address(), dsh.address(), dt.address(), dl.address(), scale, &o,
+                    dout.address(), dlse.address(), ws, ws_bytes, on.stream());
+  });
+  if (st != PAD_OK) return PyLong_FromLong(st);
+  on.used(a, n);
   PyObject *x = wrap(out), *y = wrap(lse);
   PyObject *r = x != nullptr && y != nullptr ? PyTuple_Pack(2, x, y) : nullptr;
   Py_XDECREF(x);
