@@ -317,7 +317,7 @@ def pad_decode_with_workspace(q, k_cache, v_cache, block_tables, seq_lens, scale
     _raise(st)
 
 
-# The calls below go through _pad_torch.so (csrc/pad_torch.cpp), which packs the
+# The calls below go through _pad_torch.*.so (csrc/pad_torch.cpp), which packs the
 # descriptors and allocates the outputs: a decode step makes several of them per
 # layer, and marshalling them from here costs more than their launches.  On a
 # ``stream`` other than torch's current one they allocate what they return on that
@@ -332,7 +332,9 @@ def _load_fast():
     global _fast
     if _fast is not None:
         return _fast
-    path = os.path.join(_HERE, "_pad_torch.so")
+    from ._build import binding_path
+
+    path = binding_path()
     if not os.path.exists(path):
         raise RuntimeError(f"{path} is missing: build it with `python -m paged_kv_attention_partition_b200._build`")
     lib = load_library()

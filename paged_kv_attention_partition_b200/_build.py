@@ -1,5 +1,5 @@
 """Builds libpad.so in-tree with nvcc for sm_100a (cross-compiles without a GPU),
-and _pad_torch.so, the binding's argument marshalling, with g++."""
+and the binding's argument marshalling for this torch (_pad_torch.*.so) with g++."""
 from __future__ import annotations
 
 import glob
@@ -13,7 +13,6 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libpad.so")
-BINDING = os.path.join(PKG, "_pad_torch.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]
 SOURCES = ["pad_api.cpp", "pad_rows_api.cpp", "pad_shared_api.cpp", "pad_partition.cu", "pad_umma.cu", "pad_no_alloc.cu",
@@ -46,6 +45,14 @@ def compile_command(out: str, extra=()):
             "-I", INCLUDE, "-I", CSRC, *extra, "-o", out] + [os.path.join(CSRC, s) for s in SOURCES]
 
 
+def binding_path() -> str:
+    """The binding's module for this Python and torch: a module of another torch may
+    not load, or may load and read its tensors wrongly, so each has a name of its own."""
+    import torch
+
+    return os.path.join(PKG, f"_pad_torch.{sys.implementation.cache_tag}-torch{torch.__version__}.so")
+
+
 def binding_command(out: str):
     import sysconfig
 
@@ -60,22 +67,34 @@ def binding_command(out: str):
 
 
 def build_binding(force: bool = False) -> str:
-    """Compile _pad_torch.so if its source or pad.h is newer (or force)."""
+    """Compile the binding's module if its source or pad.h is newer (or force)."""
+    path = binding_path()
     inputs = [os.path.join(CSRC, "pad_torch.cpp"), os.path.join(INCLUDE, "pad.h"), os.path.abspath(__file__)]
-    if not force and os.path.exists(BINDING) and all(os.path.getmtime(f) <= os.path.getmtime(BINDING) for f in inputs):
-        return BINDING
-    tmp = BINDING + f".tmp{os.getpid()}"
+    if not force and os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in inputs):
+        return path
+    tmp = path + f".tmp{os.getpid()}"
     cmd = binding_command(tmp)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("g++ failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
-    os.replace(tmp, BINDING)
-    return BINDING
+    os.replace(tmp, path)
+    return path
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile libpad.so (and the binding's module) if any source is newer (or force)."""
+    """Compile libpad.so, and then the binding's module where there is a torch to bind
+    to, if any source is newer (or force)."""
+    build_library(force, verbose)
+    try:
+        import torch  # noqa: F401
+    except ImportError:
+        return LIB
     build_binding(force)
+    return LIB
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
+    """Compile libpad.so, which needs neither torch nor Python, if any source is newer (or force)."""
     if not force and not is_stale():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
