@@ -122,6 +122,35 @@ __device__ __forceinline__ uint32_t max_abs(uint32_t m, const uint4 &c) {
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }
 
+// A piece's sums (a lane's row of tensor memory, 1 / l, lse) joined with what the row's
+// earlier pieces left in its part row, by a whole warp.  Pieces without a weight, lse =
+// -inf, add nothing.  A function of its own: units of one piece do not fetch it.
+template <int D>
+__device__ __noinline__ void fold_sums(uint32_t ocol, float4 *dst, float *lse_at, bool some, float lse, float inv) {
+  const float had = some ? *lse_at : -INFINITY;
+  const float top = fmaxf(had, lse), ref = top == -INFINITY ? 0.f : top;
+  const float a = exp2f(had - ref), b = exp2f(lse - ref);  // (NaN stays NaN)
+  const float keep = had == -INFINITY ? 0.f : a / (a + b);
+  inv = lse == -INFINITY ? 0.f : inv * b / (a + b);
+#pragma unroll 1
+  for (int i = 0; i < D; i += 16) {
+    float o[16];
+    tc::ld16(ocol + i, o);
+    tc::wait_ld16(o);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      if (!some) break;
+      float4 v = make_float4(o[4 * x] * inv, o[4 * x + 1] * inv, o[4 * x + 2] * inv, o[4 * x + 3] * inv);
+      if (keep != 0.f) {
+        const float4 w = dst[i / 4 + x];
+        v = make_float4(v.x + keep * w.x, v.y + keep * w.y, v.z + keep * w.z, v.w + keep * w.w);
+      }
+      dst[i / 4 + x] = v;
+    }
+  }
+  if (some) *lse_at = top + log2f(a + b);
+}
+
 template <int D, bool F8>
 __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
     shared_kernel(const __grid_constant__ SharedParams p) {
@@ -637,21 +666,25 @@ __global__ void __launch_bounds__(SharedCfg<D, F8>::kThreads, 1)
         ok = __all_sync(0xffffffffu, wait(pv_done + 8 * (n % NBUF), n / NBUF & 1));
         if (ok && live) {
           tc::fence_after();
-          const float inv = 1.f / l;
+          const float inv = 1.f / l, lse = m - C::kRaise + log2f(l);
           const int64_t row = u.part + (two || NACC == 1 ? 0 : (int64_t)j0 * u.rows) + r;
           float4 *dst = reinterpret_cast<float4 *>(p.o_part + row * D);
+          if (__builtin_expect(u.fold, 0)) {
+            fold_sums<D>(ocol, dst, p.lse_part + row, r < u.rows, lse, inv);
+          } else {
 #pragma unroll 1
-          for (int i = 0; i < D; i += 32) {
-            float o[32];
-            tc::ld32(ocol + i, o);
-            tc::wait_ld32(o);
-            if (r < u.rows) {
+            for (int i = 0; i < D; i += 32) {
+              float o[32];
+              tc::ld32(ocol + i, o);
+              tc::wait_ld32(o);
+              if (r < u.rows) {
 #pragma unroll
-              for (int x = 0; x < 8; ++x)
-                dst[i / 4 + x] = make_float4(o[4 * x] * inv, o[4 * x + 1] * inv, o[4 * x + 2] * inv, o[4 * x + 3] * inv);
+                for (int x = 0; x < 8; ++x)
+                  dst[i / 4 + x] = make_float4(o[4 * x] * inv, o[4 * x + 1] * inv, o[4 * x + 2] * inv, o[4 * x + 3] * inv);
+              }
             }
+            if (r < u.rows) p.lse_part[row] = lse;
           }
-          if (r < u.rows) p.lse_part[row] = m - C::kRaise + log2f(l);
           tc::fence_before();
         }
         __syncwarp();

@@ -10,8 +10,8 @@ struct SharedUnit {
   int32_t rest;         // 0: prefix, 1: rest
   int32_t kvh, ht;
   int32_t b0, nb;       // sequences b0 .. b0 + nb - 1
-  int32_t rows;         // nb * (heads of the tile)
-  int32_t heads;        // heads of the tile
+  int32_t rows;         // nb * gt
+  int32_t fold;         // 1: a later piece of a long unit, added to what the part rows hold
   int32_t tok0, tok1;   // tokens, tok0 a chunk's start
   int32_t chunks;
   int64_t part;         // first part row
@@ -66,12 +66,23 @@ __device__ __forceinline__ int shared_cut(const SharedParams &p, int64_t at, int
   return c > chunks ? chunks : (int)c;
 }
 
-// Calls emit(unit) for each unit of CTA `cta`, in order; all lanes of a warp
-// call it together, and emit is called by all of them with the same unit.
+// Calls emit(unit) for each unit of CTA `cta`, in order, a long one in pieces of
+// kSharedPiece chunks; all lanes of a warp call it together, and emit is called by all of
+// them with the same unit.
 template <int D, class Emit>
 __device__ __forceinline__ void shared_walk(const SharedParams &p, int cta, Emit &&emit) {
   constexpr int CT = kSharedChunk;
   const int lane = threadIdx.x & 31;
+  auto pieces = [&](SharedUnit &u) {
+    const int chunks = u.chunks, tok0 = u.tok0, tok1 = u.tok1;
+    for (int c = 0; c < chunks; c += kSharedPiece) {
+      u.fold = c > 0;
+      u.chunks = min(kSharedPiece, chunks - c);
+      u.tok0 = tok0 + c * CT;
+      u.tok1 = min(tok1, u.tok0 + u.chunks * CT);
+      emit(u);
+    }
+  };
   const SharedPrefix pre = shared_prefix(p);
   const int Lp = p.n_shared << p.bs_log2;
   const int hh = p.Hkv * p.HT;
@@ -112,7 +123,6 @@ __device__ __forceinline__ void shared_walk(const SharedParams &p, int cta, Emit
     u.ht = grp % p.HT;
     u.b0 = rb * p.nseq;
     u.nb = rb == p.nrb - 1 ? pre.last_nb : p.nseq;
-    u.heads = min(p.gt, p.g - u.ht * p.gt);
     u.rows = u.nb * p.gt;
     const int w = u.rows > kTileRows ? p.w_pre2 : p.w_pre1;
     const int c0 = shared_cut(p, pos - start, w, pre.chunks), c1 = shared_cut(p, end - start, w, pre.chunks);
@@ -120,7 +130,7 @@ __device__ __forceinline__ void shared_walk(const SharedParams &p, int cta, Emit
     u.tok1 = min(c1 * CT, Lp);
     u.chunks = c1 - c0;
     u.part = ((int64_t)grp * p.nrb + rb + cta) * p.pre_rows;
-    if (c1 > c0) emit(u);
+    if (c1 > c0) pieces(u);
     pos = start + (rb == p.nrb - 1 ? pre.last : pre.full);
   }
 
@@ -154,14 +164,13 @@ __device__ __forceinline__ void shared_walk(const SharedParams &p, int cta, Emit
         u.ht = k % p.HT;
         u.b0 = b0 + j;
         u.nb = 1;
-        u.heads = min(p.gt, p.g - u.ht * p.gt);
         u.rows = p.gt;
         const int c0 = shared_cut(p, pos - start, p.w_rest, chunks), c1 = shared_cut(p, end - start, p.w_rest, chunks);
         u.tok0 = Lp + c0 * CT;
         u.tok1 = min(Lp + c1 * CT, Lj);
         u.chunks = c1 - c0;
         u.part = p.rest_row0 + (((int64_t)u.b0 * hh + k) + cta) * p.rest_rows;
-        if (c1 > c0) emit(u);
+        if (c1 > c0) pieces(u);
         pos = start + it;
       }
     }

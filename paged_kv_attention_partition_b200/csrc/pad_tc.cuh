@@ -123,7 +123,9 @@ __host__ __device__ constexpr uint32_t idesc(int n, bool b_mn_major, bool f16) {
 
 constexpr uint32_t kNegateA = 1u << 13;  // of the instruction descriptor: -A
 
-constexpr uint64_t kWaitNs = 1000000000ull;  // no wait can legitimately take 1 s
+// No wait can legitimately take 1 s: the longest are for another role's piece of at most
+// kSharedPiece chunks, a millisecond or two each, a few of them queued.
+constexpr uint64_t kWaitNs = 1000000000ull;
 
 // Waits for the phase of `bar` with this parity, at most kWaitNs; gives up at
 // once when another role has given up, unless `drain` (the waits that make sure
