@@ -59,20 +59,24 @@ namespace {
 // weights before that, in fp32, as O and the partials are.
 //
 // Measured on B200 (bf16 unless said; merge included):
-//   256 sequences of 32 / 8 heads of 128 behind 32768 tokens: 142 us, 970 TFLOP/s, 58 %
-//     of the measured matrix peak; 64 of 40 / 8, 8192 tokens of their own each: 335 us,
-//     6.4 TB/s, 98 % of the measured copy rate.  The first is bound by the chain scores ->
-//     exponentials -> product of two tiles taking turns (tensor pipe 30 to 60 % busy, the
-//     exponentials' pipe about half), the second by HBM.
+//   256 sequences of 32 / 8 heads of 128 behind 32768 tokens: 145 us, 945 TFLOP/s, 57 %
+//     of the measured matrix peak; 64 of 40 / 8, 8192 tokens of their own each: 344 us,
+//     6.2 TB/s, 95 % of the measured copy rate.  The first is bound by the chain scores ->
+//     exponentials -> product of two tiles taking turns, the second by HBM.  With up to 400
+//     tokens behind the first's prefix (198 us) the tensor pipe is busy 40 %, the
+//     exponentials' 35 %, issue slots 32 %, DRAM 45 %: 745 MB are read where 346 would do, as
+//     row blocks cut at different chunks read a page at different times.
 //   Two buffers of 128 tokens with two threads per row 161 us where this kernel, then,
 //     took 153; a quarter of the exponentials on the FMA pipe instead of ex2 154, half
 //     163; a pair of issuing warps per accumulator the same within 1 %.
 //   Rest items (a few rows, a few chunks) are bound by latency and by instruction
 //     fetches: a unit change runs every role's code, and warps then wait for instructions
-//     longer than for anything but data.  Scores read from tensor memory twice, a half at
+//     longer than for anything but data (64 sequences with up to 700 tokens behind 8192:
+//     tensor pipe 23 %, exponentials' 14 %, DRAM 33 %).  Scores read from tensor memory twice, a half at
 //     a time in loops that are not unrolled, instead of once into 64 registers: 256
 //     sequences with up to 400 tokens behind those 32768 206 -> 195 us.
-//   E4M3, 48 sequences of 32 / 8 heads behind 6000 tokens: 43 us, of which q's conversion
+//   E4M3, 48 sequences of 32 / 8 heads behind 6000 tokens: 44 us (tensor pipe 14 %, DRAM
+//     11 %), of which q's conversion
 //     with a thread per row took 10 and two widening warps per ring instead of four 2.
 template <int D, bool F8>
 struct SharedCfg {
@@ -898,7 +902,9 @@ cudaError_t launch_t(const SharedParams &p, cudaStream_t s) {
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, shared_kernel<D, F8>, p)) != cudaSuccess) return e;
   // Two elements a lane, so more warps for a row, each with more of its partials in
-  // flight, while all the warps fit the SMs at once; four beyond.  Two against four: 24
+  // flight, while all the warps fit the SMs at once (24 each: three CTAs of 80 registers a
+  // thread at head_dim 64 and 128, and at 256, where 94 allow two, the sizes below gain
+  // with the same bound); four beyond.  Two against four: 24
   // sequences of 16 heads of 256 31.7 / 32.5 us in all, 48 of 32 of 128 43.1 / 44.2;
   // 64 of 40 of 128 52.6 / 49.7, 131 of 32 40.5 / 37.8.
   constexpr int kWide = D == 64 ? 2 : 4, kFine = 2;
