@@ -11,10 +11,10 @@
 #include <string.h>
 
 #include <atomic>
+#include <exception>
 #include <map>
 #include <set>
 #include <mutex>
-#include <new>
 #include <string>
 #include <thread>
 #include <tuple>
@@ -667,19 +667,19 @@ pad_status host_scratch(int device, cudaStream_t stream, size_t bytes, ScratchHo
   std::shared_ptr<Scratch> entry;
   try {
     do {
+      hold->lock = std::unique_lock<std::mutex>();
       {
         std::lock_guard<std::mutex> lock(g_ws_mu);
         std::shared_ptr<Scratch> &at = g_scratch[StreamKey(device, stream)];
         if (at == nullptr) at = std::make_shared<Scratch>();
         entry = at;
       }
-      if (hold->lock.owns_lock()) hold->lock.unlock();
       hold->owner = entry;
       hold->lock = std::unique_lock<std::mutex>(entry->mu);
     } while (entry->released);  // by a release between the two locks
     entry->kept.reserve(entry->kept.size() + 1);
-  } catch (const std::bad_alloc &) {
-    return fail(PAD_ERR_WORKSPACE, "out of host memory");
+  } catch (const std::exception &x) {  // (no memory for the entry, or no lock)
+    return fail(PAD_ERR_WORKSPACE, "scratch: %s", x.what());
   }
   Scratch &s = *entry;
   const unsigned long long before = s.ws.id;

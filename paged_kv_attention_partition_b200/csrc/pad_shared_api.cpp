@@ -56,8 +56,8 @@ Layout layout(const Shape &s, int ctas, pad::SharedParams *p) {
   // sequences of 40 / 8 heads behind 8192 tokens and 256 of 32 / 8 behind 32768:
   // 30 / 11 / 20 / 11 51.9 and 196 us, 40 / 11 / 20 / 9 49.8 and 196, 20 / 11 / 20 / 9
   // 47.8 and 225: the shapes pull apart (equal cuts keep row blocks of a long prefix in
-  // step, cheap items spread short rests), and these are between.  E4M3, 48 sequences of 32 / 8 heads behind 6000 tokens: 80 / 14 / 26 / 18
-  // 46.7 us, 60 / 14 / 26 / 14 43.3.
+  // step, cheap items spread short rests), and these are between.  E4M3, 48 sequences of
+  // 32 / 8 heads behind 6000 tokens: 80 / 14 / 26 / 18 46.7 us, 60 / 14 / 26 / 14 43.3.
   p->w_item = s.fp8 ? 60 : 40;
   p->w_pre1 = s.fp8 ? 14 : 11;
   p->w_pre2 = s.fp8 ? 26 : 20;

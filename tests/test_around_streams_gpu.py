@@ -151,3 +151,29 @@ def test_the_per_thread_stream_takes_given_outputs_only(cuda_device):
     got, _ = pad.pad_qk_norm_rope(x, None, q_out=out, stream=PER_THREAD)
     torch.cuda.synchronize()
     assert got is out and torch.equal(out, x)
+
+
+@pytest.mark.parametrize("mode", ["global", "thread_local", "relaxed"])
+def test_a_call_beside_a_capture_on_another_stream(cuda_device, mode):
+    # what the call asks about its own stream must not end the other's capture
+    batches = [Batch(6, 8, 2, 128, 16, 20, [5 * i for i in range(6)], seed=s) for s in (48, 49)]
+    args = [b.device(cuda_device) for b in batches]
+    for a in args:
+        a["out"] = torch.empty_like(a["q"])
+        a["lse"] = torch.empty(a["q"].shape[:2], device=cuda_device)
+    captured, others = torch.cuda.Stream(), (torch.cuda.Stream(), torch.cuda.default_stream())
+    for s in (captured, *others):  # scratch exists
+        pad.pad_decode_shared(**args[0], stream=s)
+    torch.cuda.synchronize()
+    for other in others:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=captured, capture_error_mode=mode):
+            pad.pad_decode_shared(**args[0])
+            pad.pad_decode_shared(**args[1], stream=other)
+            pad.pad_decode_shared(**args[0])
+        torch.cuda.synchronize()
+        check(args[1]["out"], args[1]["lse"], batches[1].reference(), "beside")
+        args[0]["out"].fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        check(args[0]["out"], args[0]["lse"], batches[0].reference(), "captured")
